@@ -253,7 +253,8 @@ def _norm_backward(s):
 
 def _i8_product(s):
     x = s["x"].float()
-    xs = x.abs().amax(1) / 127.0
+    xs = x.abs().amax(1)
+    xs = xs / torch.full_like(xs, 127.0)  # a tensor: by a number, torch multiplies with its rounded inverse
     q = torch.clamp(torch.round(torch.nan_to_num(x / xs[:, None])), -127, 127)
     y = (q @ s["wq"].float().t()) * xs[:, None] * s["ws"]
     if s["bias"] is not None:
