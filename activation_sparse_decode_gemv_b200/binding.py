@@ -26,13 +26,22 @@ PI_W_F32, PI_W_F16, PI_W_INT4G32 = 0, 1, 2
 PI_FFN_ACCUMULATE, PI_FFN_HOT_DENSE, PI_FFN_HOT_INDEX = 1, 2, 4
 PI_STATIC_SCRATCH_BYTES = 16 * 1024 * 1024  # device scratch of pi_decode_ffn_static
 
+PI_DT_F32, PI_DT_F16, PI_DT_BF16 = 0, 1, 2
+PI_GATE_SILU, PI_GATE_RELU, PI_GATE_GELU = 0, 1, 2
+PI_GRAD_ACCUMULATE = 1
+
 WTYPE = {"f32": PI_W_F32, "f16": PI_W_F16, "int4g32": PI_W_INT4G32}
 ACT = {"relu": PI_ACT_RELU, "swiglu": PI_ACT_SWIGLU}
+DTYPE = {torch.float32: PI_DT_F32, torch.float16: PI_DT_F16, torch.bfloat16: PI_DT_BF16}
+GATE_ACT = {"silu": PI_GATE_SILU, "relu": PI_GATE_RELU, "gelu": PI_GATE_GELU}
 
 # every symbol the header declares
 EXPORTS = ("pi_ffn_create", "pi_ffn_destroy", "pi_workspace_size", "pi_workspace_init", "pi_predict",
            "pi_sparse_ffn", "pi_decode_ffn", "pi_decode_ffn_stack", "pi_decode_ffn_static", "pi_debug_wait_fault",
-           "pi_get_device_status", "pi_status_string")
+           "pi_get_device_status", "pi_status_string",
+           "pi_gated_ffn_create", "pi_gated_ffn_destroy", "pi_gated_ffn_workspace_size", "pi_gated_ffn_forward",
+           "pi_gated_ffn_backward", "pi_block_norm_forward", "pi_block_norm_workspace_size",
+           "pi_block_norm_backward", "pi_quantize_i8", "pi_matmul_i8_workspace_size", "pi_matmul_i8")
 
 
 class PiError(RuntimeError):
@@ -47,6 +56,17 @@ class pi_ffn_desc(C.Structure):
                 ("w_up", C.c_void_p), ("w_gate", C.c_void_p), ("w_down_t", C.c_void_p),
                 ("s_up", C.c_void_p), ("s_gate", C.c_void_p), ("s_down_t", C.c_void_p),
                 ("b_up", C.c_void_p), ("p1", C.c_void_p), ("p2", C.c_void_p), ("p_bias", C.c_void_p)]
+
+
+class pi_gated_ffn_desc(C.Structure):
+    _fields_ = [("d_model", C.c_int), ("d_ffn", C.c_int), ("act", C.c_int), ("dtype", C.c_int),
+                ("w_gate", C.c_void_p), ("w_up", C.c_void_p), ("w_down_t", C.c_void_p)]
+
+
+class pi_block_norm_desc(C.Structure):
+    _fields_ = [("d_model", C.c_int), ("y_dtype", C.c_int), ("u_dtype", C.c_int), ("post_norm", C.c_int),
+                ("eps", C.c_float), ("residual_scale", C.c_float), ("branch_scale", C.c_float),
+                ("w_post", C.c_void_p), ("w_pre", C.c_void_p), ("gate", C.c_void_p), ("tokens_per_gate", C.c_int)]
 
 
 _lib = None
@@ -75,6 +95,23 @@ def lib() -> C.CDLL:
         L.pi_get_device_status.argtypes = [vp, vp, C.POINTER(i)]
         L.pi_status_string.argtypes = [i]
         L.pi_status_string.restype = C.c_char_p
+        L.pi_gated_ffn_create.argtypes = [C.POINTER(pi_gated_ffn_desc), C.POINTER(vp)]
+        L.pi_gated_ffn_destroy.argtypes = [vp]
+        L.pi_gated_ffn_destroy.restype = None
+        L.pi_gated_ffn_workspace_size.argtypes = [vp, i, i, C.POINTER(sz)]
+        L.pi_gated_ffn_forward.argtypes = [vp, vp, i, vp, vp, vp, vp, sz, vp]
+        L.pi_gated_ffn_backward.argtypes = [vp, vp, vp, vp, vp, i, vp, vp, vp, vp, i, C.c_uint, vp, sz, vp]
+        nd = C.POINTER(pi_block_norm_desc)
+        L.pi_block_norm_forward.argtypes = [nd, vp, vp, i, vp, vp, vp, vp, vp]
+        L.pi_block_norm_workspace_size.argtypes = [nd, i, C.POINTER(sz)]
+        L.pi_block_norm_backward.argtypes = [nd] + [vp] * 6 + [i] + [vp] * 5 + [C.c_uint, vp, sz, vp]
+        L.pi_quantize_i8.argtypes = [vp, i, i, i, vp, vp, vp]
+        L.pi_matmul_i8_workspace_size.argtypes = [i, i, i, C.POINTER(sz)]
+        L.pi_matmul_i8.argtypes = [vp, vp, vp, vp, vp, i, i, i, vp, i, vp, sz, vp]
+        for n in ("pi_gated_ffn_create", "pi_gated_ffn_workspace_size", "pi_gated_ffn_forward",
+                  "pi_gated_ffn_backward", "pi_block_norm_forward", "pi_block_norm_workspace_size",
+                  "pi_block_norm_backward", "pi_quantize_i8", "pi_matmul_i8_workspace_size", "pi_matmul_i8"):
+            getattr(L, n).restype = C.c_int
         for n in ("pi_ffn_create", "pi_workspace_size", "pi_workspace_init", "pi_predict", "pi_sparse_ffn",
                   "pi_decode_ffn", "pi_decode_ffn_stack", "pi_decode_ffn_static", "pi_debug_wait_fault",
                   "pi_get_device_status"):
@@ -280,3 +317,256 @@ def pi_get_device_status(ws: torch.Tensor, stream=None) -> int:
     code = C.c_int()
     _check(lib().pi_get_device_status(_p(ws), _stream(stream), C.byref(code)), "pi_get_device_status")
     return code.value
+
+
+# ---------------------------------------------------------------- dense block operators
+def _check_out(t: Optional[torch.Tensor], what: str, dtype, shape):
+    """An exactly shaped contiguous tensor (None passes)."""
+    if t is None:
+        return
+    if t.dtype != dtype:
+        raise ValueError(f"{what}: dtype {t.dtype}, expected {dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what}: must be contiguous")
+
+
+def _one_device(**tensors: Optional[torch.Tensor]):
+    """All tensors on the current CUDA device: kernels launch there, on its current stream."""
+    _on_device(**tensors)
+    for what, t in tensors.items():
+        if t is not None and t.device.index != torch.cuda.current_device():
+            raise ValueError(f"{what}: on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
+
+
+def _zeroed_workspace(n: int, device=None) -> torch.Tensor:
+    ws = torch.empty(n, dtype=torch.uint8, device=device or torch.device("cuda"))
+    ws[:256].zero_()
+    return ws
+
+
+class GatedFfnLayer:
+    """A created pi_gated_ffn handle plus references to the weights it borrows
+    (each [f, d], fp16 or bf16, contiguous)."""
+
+    def __init__(self, w_gate: torch.Tensor, w_up: torch.Tensor, w_down_t: torch.Tensor, *, act: str = "silu"):
+        if w_gate.dim() != 2 or w_gate.dtype not in (torch.float16, torch.bfloat16):
+            raise ValueError(f"w_gate: {w_gate.dtype} of shape {tuple(w_gate.shape)}, expected fp16 or bf16 [f, d]")
+        if act not in GATE_ACT:
+            raise ValueError(f"act: {act!r}, expected one of {sorted(GATE_ACT)}")
+        self.f, self.d = w_gate.shape
+        self.dtype, self.act = w_gate.dtype, act
+        for what, t in (("w_gate", w_gate), ("w_up", w_up), ("w_down_t", w_down_t)):
+            _check_out(t, what, self.dtype, (self.f, self.d))
+            if t.device != w_gate.device:
+                raise ValueError(f"{what}: on {t.device}, w_gate is on {w_gate.device}")
+        self._keep = (w_gate, w_up, w_down_t)
+        self.desc = pi_gated_ffn_desc(self.d, self.f, GATE_ACT[act], DTYPE[self.dtype], _p(w_gate), _p(w_up),
+                                      _p(w_down_t))
+        h = C.c_void_p()
+        _check(lib().pi_gated_ffn_create(C.byref(self.desc), C.byref(h)), "pi_gated_ffn_create")
+        self.handle = h
+
+    def close(self):
+        if getattr(self, "handle", None):
+            lib().pi_gated_ffn_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def pi_gated_ffn_workspace_size(layer: GatedFfnLayer, max_tokens: int, backward: bool = False) -> int:
+    n = C.c_size_t()
+    _check(lib().pi_gated_ffn_workspace_size(layer.handle, int(max_tokens), int(backward), C.byref(n)),
+           "pi_gated_ffn_workspace_size")
+    return n.value
+
+
+def make_gated_ffn_workspace(layer: GatedFfnLayer, max_tokens: int, backward: bool = False, device=None):
+    """Allocate (with torch) a workspace for calls of up to max_tokens tokens."""
+    return _zeroed_workspace(pi_gated_ffn_workspace_size(layer, max_tokens, backward), device)
+
+
+def pi_gated_ffn_forward(layer: GatedFfnLayer, u: torch.Tensor, y: torch.Tensor, ws: torch.Tensor,
+                         gate: Optional[torch.Tensor] = None, up: Optional[torch.Tensor] = None, stream=None):
+    """u [T, d] -> y [T, d]; gate, up: optional outputs [T, f] (the pre-activations)."""
+    T = _tokens(u, layer.d, "u")
+    _check_out(u, "u", layer.dtype, (T, layer.d))
+    _check_out(y, "y", layer.dtype, (T, layer.d))
+    _check_out(gate, "gate", layer.dtype, (T, layer.f))
+    _check_out(up, "up", layer.dtype, (T, layer.f))
+    _need_ws(ws)
+    _one_device(u=u, y=y, gate=gate, up=up, workspace=ws, weights=layer._keep[0])
+    _check(lib().pi_gated_ffn_forward(layer.handle, _p(u), T, _p(y), _p(gate), _p(up), *_wsargs(ws),
+                                      _stream(stream)), "pi_gated_ffn_forward")
+
+
+def pi_gated_ffn_backward(layer: GatedFfnLayer, u: torch.Tensor, gate: torch.Tensor, up: torch.Tensor,
+                          dy: torch.Tensor, ws: torch.Tensor, du: Optional[torch.Tensor] = None,
+                          dw_gate: Optional[torch.Tensor] = None, dw_up: Optional[torch.Tensor] = None,
+                          dw_down_t: Optional[torch.Tensor] = None, flags: int = 0, stream=None):
+    """Gradients at a forward call's u, gate and up, for dy [T, d].  du [T, d];
+    dw_* [f, d], all fp32 or all of the layer's type; each may be left out."""
+    T = _tokens(u, layer.d, "u")
+    for what, t in (("u", u), ("dy", dy), ("du", du)):
+        _check_out(t, what, layer.dtype, (T, layer.d))
+    for what, t in (("gate", gate), ("up", up)):
+        _check_out(t, what, layer.dtype, (T, layer.f))
+    gtype = next((t.dtype for t in (dw_gate, dw_up, dw_down_t) if t is not None), layer.dtype)
+    if gtype not in (torch.float32, layer.dtype):
+        raise ValueError(f"dw_*: dtype {gtype}, expected torch.float32 or {layer.dtype}")
+    for what, t in (("dw_gate", dw_gate), ("dw_up", dw_up), ("dw_down_t", dw_down_t)):
+        _check_out(t, what, gtype, (layer.f, layer.d))
+    _need_ws(ws)
+    _one_device(u=u, gate=gate, up=up, dy=dy, du=du, dw_gate=dw_gate, dw_up=dw_up, dw_down_t=dw_down_t, workspace=ws,
+                weights=layer._keep[0])
+    _check(lib().pi_gated_ffn_backward(layer.handle, _p(u), _p(gate), _p(up), _p(dy), T, _p(du), _p(dw_gate),
+                                       _p(dw_up), _p(dw_down_t), DTYPE[gtype], int(flags), *_wsargs(ws),
+                                       _stream(stream)), "pi_gated_ffn_backward")
+
+
+class BlockNorm:
+    """The parameters of the norms around a block (see pi_block_norm_desc) and
+    references to the tensors they borrow.  w_post, w_pre: fp32 [d] or None;
+    gate: fp32 [rows, d] or None, row t // tokens_per_gate for token t."""
+
+    def __init__(self, d: int, *, y_dtype=torch.float16, u_dtype=torch.float16, eps: float = 1e-6,
+                 residual_scale: float = 1.0, branch_scale: float = 1.0, post_norm: bool = False,
+                 w_post: Optional[torch.Tensor] = None, w_pre: Optional[torch.Tensor] = None,
+                 gate: Optional[torch.Tensor] = None, tokens_per_gate: int = 0):
+        for what, t in (("y_dtype", y_dtype), ("u_dtype", u_dtype)):
+            if t not in DTYPE:
+                raise ValueError(f"{what}: {t}, expected one of {list(DTYPE)}")
+        _check_out(w_post, "w_post", torch.float32, (d,))
+        _check_out(w_pre, "w_pre", torch.float32, (d,))
+        if gate is not None:
+            if gate.dim() != 2 or int(tokens_per_gate) <= 0:
+                raise ValueError("gate: expected [rows, d] and tokens_per_gate > 0")
+            _check_out(gate, "gate", torch.float32, (gate.shape[0], d))
+        self.d, self.y_dtype, self.u_dtype, self.post_norm = d, y_dtype, u_dtype, bool(post_norm)
+        self.gate, self.tokens_per_gate = gate, int(tokens_per_gate)
+        self.w_post, self.w_pre = w_post, w_pre
+        self.desc = pi_block_norm_desc(d, DTYPE[y_dtype], DTYPE[u_dtype], int(post_norm), eps, residual_scale,
+                                       branch_scale, _p(w_post), _p(w_pre), _p(gate), int(tokens_per_gate))
+
+    def _check_tokens(self, T: int):
+        """The gate has a row for each of T tokens."""
+        if self.gate is not None and self.gate.shape[0] * self.tokens_per_gate < T:
+            raise ValueError(f"gate: {self.gate.shape[0]} rows of {self.tokens_per_gate} tokens for {T} tokens")
+
+
+def pi_block_norm_forward(norm: BlockNorm, x: torch.Tensor, y: Optional[torch.Tensor],
+                          x_out: Optional[torch.Tensor], u: Optional[torch.Tensor],
+                          rstd_post: Optional[torch.Tensor] = None, rstd_pre: Optional[torch.Tensor] = None,
+                          stream=None):
+    """x fp32 [T, d] and y [T, d] -> the new stream x_out fp32 [T, d] (may be x)
+    and the next block's input u [T, d]; rstd_post, rstd_pre: optional fp32 [T]."""
+    T = _tokens(x, norm.d, "x")
+    norm._check_tokens(T)
+    _check_out(x, "x", torch.float32, (T, norm.d))
+    _check_out(y, "y", norm.y_dtype, (T, norm.d))
+    _check_out(x_out, "x_out", torch.float32, (T, norm.d))
+    _check_out(u, "u", norm.u_dtype, (T, norm.d))
+    _check_out(rstd_post, "rstd_post", torch.float32, (T,))
+    _check_out(rstd_pre, "rstd_pre", torch.float32, (T,))
+    _one_device(x=x, y=y, x_out=x_out, u=u, rstd_post=rstd_post, rstd_pre=rstd_pre, w_post=norm.w_post,
+                w_pre=norm.w_pre, gate=norm.gate)
+    _check(lib().pi_block_norm_forward(C.byref(norm.desc), _p(x), _p(y), T, _p(x_out), _p(u), _p(rstd_post),
+                                       _p(rstd_pre), _stream(stream)), "pi_block_norm_forward")
+
+
+def pi_block_norm_workspace_size(norm: BlockNorm, max_tokens: int) -> int:
+    n = C.c_size_t()
+    _check(lib().pi_block_norm_workspace_size(C.byref(norm.desc), int(max_tokens), C.byref(n)),
+           "pi_block_norm_workspace_size")
+    return n.value
+
+
+def make_block_norm_workspace(norm: BlockNorm, max_tokens: int, device=None):
+    """Allocate (with torch) a workspace for backward calls of up to max_tokens tokens."""
+    return _zeroed_workspace(pi_block_norm_workspace_size(norm, max_tokens), device)
+
+
+def pi_block_norm_backward(norm: BlockNorm, x_out: Optional[torch.Tensor], y: Optional[torch.Tensor],
+                           rstd_post: Optional[torch.Tensor], rstd_pre: Optional[torch.Tensor],
+                           du: Optional[torch.Tensor], dx_out: Optional[torch.Tensor], dx: Optional[torch.Tensor],
+                           dy: Optional[torch.Tensor], ws: torch.Tensor, dw_post: Optional[torch.Tensor] = None,
+                           dw_pre: Optional[torch.Tensor] = None, dgate: Optional[torch.Tensor] = None,
+                           flags: int = 0, stream=None):
+    """Gradients for du [T, d] and dx_out fp32 [T, d] (either may be None): dx
+    fp32 [T, d] (may be dx_out), dy [T, d] (may be y), dw_post, dw_pre fp32 [d] and
+    dgate of the gate's shape; each may be left out."""
+    lead = du if du is not None else dx_out
+    if lead is None:
+        raise ValueError("pi_block_norm_backward needs du or dx_out")
+    T = _tokens(lead, norm.d, "du" if du is not None else "dx_out")
+    norm._check_tokens(T)
+    for what, t, dt in (("x_out", x_out, torch.float32), ("y", y, norm.y_dtype), ("du", du, norm.u_dtype),
+                        ("dx_out", dx_out, torch.float32), ("dx", dx, torch.float32), ("dy", dy, norm.y_dtype)):
+        _check_out(t, what, dt, (T, norm.d))
+    _check_out(rstd_post, "rstd_post", torch.float32, (T,))
+    _check_out(rstd_pre, "rstd_pre", torch.float32, (T,))
+    _check_out(dw_post, "dw_post", torch.float32, (norm.d,))
+    _check_out(dw_pre, "dw_pre", torch.float32, (norm.d,))
+    if dgate is not None:
+        if norm.gate is None:
+            raise ValueError("dgate: there is no gate")
+        _check_out(dgate, "dgate", torch.float32, norm.gate.shape)
+    _need_ws(ws)
+    _one_device(x_out=x_out, y=y, rstd_post=rstd_post, rstd_pre=rstd_pre, du=du, dx_out=dx_out, dx=dx, dy=dy,
+                workspace=ws, dw_post=dw_post, dw_pre=dw_pre, dgate=dgate, w_post=norm.w_post, w_pre=norm.w_pre,
+                gate=norm.gate)
+    _check(lib().pi_block_norm_backward(C.byref(norm.desc), _p(x_out), _p(y), _p(rstd_post), _p(rstd_pre), _p(du),
+                                        _p(dx_out), T, _p(dx), _p(dy), _p(dw_post), _p(dw_pre), _p(dgate),
+                                        int(flags), *_wsargs(ws), _stream(stream)), "pi_block_norm_backward")
+
+
+def pi_quantize_i8(x: torch.Tensor, q: torch.Tensor, scales: torch.Tensor, stream=None):
+    """Rows of x [rows, k] (fp32, fp16 or bf16) -> int8 codes q [rows, k] and fp32 scales [rows]."""
+    if x.dim() != 2 or x.dtype not in DTYPE:
+        raise ValueError(f"x: {x.dtype} of shape {tuple(x.shape)}, expected fp32, fp16 or bf16 [rows, k]")
+    rows, k = x.shape
+    _check_out(x, "x", x.dtype, (rows, k))
+    _check_out(q, "q", torch.int8, (rows, k))
+    _check_out(scales, "scales", torch.float32, (rows,))
+    _one_device(x=x, q=q, scales=scales)
+    _check(lib().pi_quantize_i8(_p(x), DTYPE[x.dtype], rows, k, _p(q), _p(scales), _stream(stream)),
+           "pi_quantize_i8")
+
+
+def pi_matmul_i8_workspace_size(tokens: int, n: int, k: int) -> int:
+    size = C.c_size_t()
+    _check(lib().pi_matmul_i8_workspace_size(int(tokens), int(n), int(k), C.byref(size)),
+           "pi_matmul_i8_workspace_size")
+    return size.value
+
+
+def make_matmul_i8_workspace(max_tokens: int, n: int, k: int, device=None):
+    """Allocate (with torch) a workspace for products of up to max_tokens tokens."""
+    return _zeroed_workspace(pi_matmul_i8_workspace_size(max_tokens, n, k), device)
+
+
+def pi_matmul_i8(xq: torch.Tensor, x_scales: torch.Tensor, wq: torch.Tensor, w_scales: torch.Tensor,
+                 y: torch.Tensor, ws: torch.Tensor, bias: Optional[torch.Tensor] = None, stream=None):
+    """xq int8 [T, k] with x_scales fp32 [T], wq int8 [n, k] with w_scales fp32
+    [n], bias fp32 [n] or None -> y [T, n] (fp32, fp16 or bf16)."""
+    if xq.dim() != 2 or wq.dim() != 2 or xq.shape[1] != wq.shape[1]:
+        raise ValueError(f"xq {tuple(xq.shape)} and wq {tuple(wq.shape)}: expected [T, k] and [n, k]")
+    if y.dtype not in DTYPE:
+        raise ValueError(f"y: dtype {y.dtype}, expected one of {list(DTYPE)}")
+    (T, k), n = xq.shape, wq.shape[0]
+    _check_out(xq, "xq", torch.int8, (T, k))
+    _check_out(wq, "wq", torch.int8, (n, k))
+    _check_out(x_scales, "x_scales", torch.float32, (T,))
+    _check_out(w_scales, "w_scales", torch.float32, (n,))
+    _check_out(bias, "bias", torch.float32, (n,))
+    _check_out(y, "y", y.dtype, (T, n))
+    _need_ws(ws)
+    _one_device(xq=xq, x_scales=x_scales, wq=wq, w_scales=w_scales, bias=bias, y=y, workspace=ws)
+    _check(lib().pi_matmul_i8(_p(xq), _p(x_scales), _p(wq), _p(w_scales), _p(bias), T, n, k, _p(y), DTYPE[y.dtype],
+                              *_wsargs(ws), _stream(stream)), "pi_matmul_i8")

@@ -1,0 +1,753 @@
+// pi_gemm.cuh -- tcgen05 matrix-product kernels of the dense operators (the
+// gated feed-forward block, its gradients, the 8-bit integer product).
+//
+// Every product is computed as D[m, n] = sum_k A[m, k] B[n, k] with the
+// FEATURE axis (neurons, channels, columns of a weight) on m, the lanes of
+// tensor memory, and the TOKEN axis on n, its columns.  Results are row-major
+// in tokens, so a warp's 32 lanes store 32 consecutive features of one token:
+// the epilogues write from registers, with no transposition.  One orientation
+// also serves every token count: n is the small MMA extent when there are few
+// tokens, and the weights always fill the 128 or 256 rows.
+//
+// Operands are 128-byte wide K blocks (64 16-bit or 128 8-bit elements),
+// brought by TMA with the 128-byte swizzle and read in place by the MMA:
+//   K-major  (row = one m or n, k contiguous):  box 64 k x R rows
+//   MN-major (row = one k, m or n contiguous):  boxes 64 m x 64 k
+// Elements outside a matrix read as zero, so ragged edges add exact zeros.
+//
+// Two kernels:
+//   pair_gemm_kernel   many tiles: CTA pairs (cta_group::2), 256 x NT tiles,
+//                      persistent, accumulators double-buffered so that the
+//                      epilogue of a tile runs under the next tile's MMAs;
+//   split_gemm_kernel  few tokens: 128 x NT tiles, K split over a cluster's
+//                      CTAs, partial sums joined through distributed shared
+//                      memory in rank order (no workspace, no atomics).
+// Every mbarrier wait is bounded; a wait that gives up records
+// PI_ERR_TIMEOUT and the kernel ends.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <stdint.h>
+
+#include "pi_umma.cuh"
+
+namespace pi {
+namespace gemm {
+
+using namespace tc;
+
+enum Epi {
+  E_STORE = 0,  // out[n, m] = D  (16-bit or fp32; optionally added to what is there)
+  E_GLU = 1,    // rows are gate | up neurons: a = phi(g) p, and optionally g and p themselves
+  E_DGLU = 2,   // D = da: dg = da p phi'(g), dp = da phi(g), a = phi(g) p
+  E_I8 = 3      // int32 D: out[n, m] = D s_n s_m + bias_m
+};
+enum GateAct { G_SILU = 0, G_RELU = 1, G_GELU = 2 };
+enum OutType { O_F32 = 0, O_F16 = 1, O_BF16 = 2 };
+
+constexpr int kMaxMaps = 3;
+
+struct Args {
+  CUtensorMap ma[kMaxMaps], mb[kMaxMaps];  // operand maps, by problem or by K segment
+  int m, n;          // extents (E_GLU: m = neurons)
+  int kb, kb_seg;    // K blocks per tile; per segment (kb = kb_seg x segments)
+  int nprob;         // independent products of the same shape (1 segment each)
+  int mt, nt;        // tiles along m and n
+  uint32_t idesc;    // MMA instruction descriptor
+  void *out[kMaxMaps];
+  long long ldo;     // elements between consecutive n of out, gate_*, up_*
+  int out_type;      // OutType
+  int accumulate;    // E_STORE: add to out
+  int act;           // GateAct
+  const void *gate_in, *up_in;  // E_DGLU
+  void *gate_out, *up_out;      // E_GLU: g, p (or null); E_DGLU: dg, dp
+  const float *s_n, *s_m, *bias;  // E_I8
+  int early_a;       // split kernel: A was written before the previous kernel; load it before that one ends
+  int *status;
+};
+
+// ---------------------------------------------------------------- PTX: clusters and CTA pairs
+PI_DEV uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+PI_DEV uint32_t mapa(uint32_t saddr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
+  return r;
+}
+// all threads of the cluster; orders shared memory accesses across it
+PI_DEV void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+PI_DEV float ld_cluster_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+PI_DEV void mbar_arrive_cluster(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+PI_DEV bool mbar_try_cluster(uint64_t *b, unsigned parity, unsigned hint_ns) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(su32(b)), "r"(parity), "r"(hint_ns)
+      : "memory");
+  return ok != 0;
+}
+// bounded wait on a barrier that the other CTA of the pair may complete
+static __device__ __noinline__ bool mbar_wait_cluster_slow(uint64_t *b, unsigned parity, volatile int *abort_flag,
+                                                           int *status) {
+  const unsigned long long t0 = now_ns();
+  for (;;) {
+    if (mbar_try_cluster(b, parity, 20000u)) return true;
+    if (*abort_flag) return false;
+    if (now_ns() - t0 > kWaitNs) {
+      set_status(status, kStatusTimeout);
+      *abort_flag = 1;
+      return false;
+    }
+  }
+}
+PI_DEV bool mbar_wait_cluster(uint64_t *b, unsigned parity, volatile int *abort_flag, int *status) {
+  if (mbar_try_cluster(b, parity, 0u)) return true;
+  return mbar_wait_cluster_slow(b, parity, abort_flag, status);
+}
+
+// TMA load into this CTA's shared memory that completes on a barrier of
+// either CTA of the pair (bar: shared::cluster address)
+PI_DEV void tma_load_2d_pair(uint32_t dst, const CUtensorMap *tm, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
+      "[%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+PI_DEV void prefetch_map(const CUtensorMap *tm) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(tm)) : "memory");
+}
+
+template <int GROUP, bool I8>
+PI_DEV void mma(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  if constexpr (GROUP == 2) {
+    if constexpr (I8)
+      asm volatile(
+          "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+          " tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+          "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+          : "memory");
+    else
+      asm volatile(
+          "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+          " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+          "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+          : "memory");
+  } else {
+    if constexpr (I8)
+      asm volatile(
+          "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+          " tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+          "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+          : "memory");
+    else
+      mma_ss(d, adesc, bdesc, idesc, accumulate);
+  }
+}
+// arrive on the same barrier of both CTAs of the pair when all MMAs issued so far are done
+PI_DEV void mma_commit_pair(uint64_t *b) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          su32(b)),
+      "h"((uint16_t)3)
+      : "memory");
+}
+PI_DEV void tmem_alloc_pair(uint32_t *slot, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32(slot)), "r"(ncols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+PI_DEV void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+
+// operand descriptor of K step j (32 bytes of k per row, or 16 k) in a stage
+template <int MN>
+PI_DEV uint64_t operand_desc(uint32_t base, int j) {
+  // K-major: 8-row groups 1 KB apart.  MN-major: 64-element blocks 8 KB
+  // apart, 8-k groups 1 KB apart.
+  return MN ? sdesc(base + j * 2048, 8192, 1024, kSw128) : sdesc(base + j * 32, 16, 1024, kSw128);
+}
+
+// ---------------------------------------------------------------- element types
+template <typename T> struct Elem;
+template <> struct Elem<__half> {
+  static PI_DEV __half from(float v) { return __float2half_rn(v); }
+  static PI_DEV float to(__half v) { return __half2float(v); }
+};
+template <> struct Elem<__nv_bfloat16> {
+  static PI_DEV __nv_bfloat16 from(float v) { return __float2bfloat16_rn(v); }
+  static PI_DEV float to(__nv_bfloat16 v) { return __bfloat162float(v); }
+};
+
+// ---------------------------------------------------------------- gate activations
+// phi and phi' in fp32; the caller rounds once.
+template <int ACT>
+PI_DEV float gate_phi(float g) {
+  if constexpr (ACT == G_SILU) return g / (1.f + __expf(-g));
+  if constexpr (ACT == G_RELU) return g < 0.f ? 0.f : g;  // NaN stays NaN
+  return 0.5f * g * (1.f + erff(g * 0.70710678f));
+}
+template <int ACT>
+PI_DEV void gate_phi_grad(float g, float &phi, float &slope) {
+  if constexpr (ACT == G_SILU) {
+    const float s = 1.f / (1.f + __expf(-g));
+    phi = g * s;
+    slope = s * (1.f + g * (1.f - s));
+  } else if constexpr (ACT == G_RELU) {
+    phi = g < 0.f ? 0.f : g;
+    slope = g > 0.f ? 1.f : 0.f;
+  } else {
+    const float c = 0.5f * (1.f + erff(g * 0.70710678f));
+    phi = g * c;
+    slope = c + g * 0.39894228f * __expf(-0.5f * g * g);
+  }
+}
+
+// ---------------------------------------------------------------- element epilogues
+// NC consecutive columns n0.. of feature m; `ok` is m < a.m.  vals: fp32 sums
+// (E_I8: int32 bits).
+template <int NC>
+PI_DEV void put_cols(const Args &a, void *out, int m, int n0, bool ok, const float (&v)[NC], int type, int acc) {
+  if (!ok) return;
+  const size_t at = (size_t)n0 * a.ldo + m;
+  if (type == O_F32) {
+    float *p = reinterpret_cast<float *>(out) + at;
+#pragma unroll
+    for (int j = 0; j < NC; ++j)
+      if (n0 + j < a.n) p[(size_t)j * a.ldo] = acc ? p[(size_t)j * a.ldo] + v[j] : v[j];
+  } else if (type == O_F16) {
+    __half *p = reinterpret_cast<__half *>(out) + at;
+#pragma unroll
+    for (int j = 0; j < NC; ++j)
+      if (n0 + j < a.n) {
+        __half *q = p + (size_t)j * a.ldo;
+        *q = __float2half_rn(acc ? __half2float(*q) + v[j] : v[j]);
+      }
+  } else {
+    __nv_bfloat16 *p = reinterpret_cast<__nv_bfloat16 *>(out) + at;
+#pragma unroll
+    for (int j = 0; j < NC; ++j)
+      if (n0 + j < a.n) {
+        __nv_bfloat16 *q = p + (size_t)j * a.ldo;
+        *q = __float2bfloat16_rn(acc ? __bfloat162float(*q) + v[j] : v[j]);
+      }
+  }
+}
+
+template <int NC, typename T>
+PI_DEV void put_t(const Args &a, void *out, int m, int n0, bool ok, const float (&v)[NC]) {
+  if (!ok) return;
+  T *p = reinterpret_cast<T *>(out) + (size_t)n0 * a.ldo + m;
+#pragma unroll
+  for (int j = 0; j < NC; ++j)
+    if (n0 + j < a.n) p[(size_t)j * a.ldo] = Elem<T>::from(v[j]);
+}
+
+template <int NC>
+PI_DEV void epi_i8(const Args &a, int m, int n0, bool ok, const float (&v)[NC]) {
+  const float sm = ok ? __ldg(a.s_m + m) : 0.f;
+  const float b = ok && a.bias ? __ldg(a.bias + m) : 0.f;
+  float o[NC];
+#pragma unroll
+  for (int j = 0; j < NC; ++j) {
+    const float sn = n0 + j < a.n ? __ldg(a.s_n + n0 + j) : 0.f;
+    o[j] = fmaf((float)__float_as_int(v[j]) * sn, sm, b);
+  }
+  put_cols<NC>(a, a.out[0], m, n0, ok, o, a.out_type, 0);
+}
+
+template <int NC, typename T, int ACT>
+PI_DEV void epi_dglu_act(const Args &a, int m, int n0, bool ok, const float (&v)[NC], const float (&g)[NC],
+                         const float (&p)[NC]) {
+  float dg[NC], dp[NC], av[NC];
+#pragma unroll
+  for (int j = 0; j < NC; ++j) {
+    float phi, slope;
+    gate_phi_grad<ACT>(g[j], phi, slope);
+    dp[j] = v[j] * phi;
+    dg[j] = v[j] * p[j] * slope;
+    av[j] = phi * p[j];
+  }
+  put_t<NC, T>(a, a.gate_out, m, n0, ok, dg);
+  put_t<NC, T>(a, a.up_out, m, n0, ok, dp);
+  put_t<NC, T>(a, a.out[0], m, n0, ok, av);
+}
+template <int NC, typename T>
+PI_DEV void load_gp(const Args &a, int m, int n0, bool ok, float (&g)[NC], float (&p)[NC]) {
+  const T *gi = reinterpret_cast<const T *>(a.gate_in) + (size_t)n0 * a.ldo + m;
+  const T *pi = reinterpret_cast<const T *>(a.up_in) + (size_t)n0 * a.ldo + m;
+#pragma unroll
+  for (int j = 0; j < NC; ++j) {
+    const bool in = ok && n0 + j < a.n;
+    g[j] = in ? Elem<T>::to(gi[(size_t)j * a.ldo]) : 0.f;
+    p[j] = in ? Elem<T>::to(pi[(size_t)j * a.ldo]) : 0.f;
+  }
+}
+template <int NC, typename T>
+PI_DEV void epi_dglu(const Args &a, int m, int n0, bool ok, const float (&v)[NC], const float (&g)[NC],
+                     const float (&p)[NC]) {
+  if (a.act == G_SILU) epi_dglu_act<NC, T, G_SILU>(a, m, n0, ok, v, g, p);
+  else if (a.act == G_RELU) epi_dglu_act<NC, T, G_RELU>(a, m, n0, ok, v, g, p);
+  else epi_dglu_act<NC, T, G_GELU>(a, m, n0, ok, v, g, p);
+}
+
+template <int NC>
+PI_DEV void glu(int act, const float (&g)[NC], const float (&p)[NC], float (&o)[NC]) {
+  if (act == G_SILU) {
+#pragma unroll
+    for (int j = 0; j < NC; ++j) o[j] = gate_phi<G_SILU>(g[j]) * p[j];
+  } else if (act == G_RELU) {
+#pragma unroll
+    for (int j = 0; j < NC; ++j) o[j] = gate_phi<G_RELU>(g[j]) * p[j];
+  } else {
+#pragma unroll
+    for (int j = 0; j < NC; ++j) o[j] = gate_phi<G_GELU>(g[j]) * p[j];
+  }
+}
+
+// K block kb of a tile -> map index (segment) and element offset along K
+PI_DEV void k_at(const Args &a, int prob, int kb, int &map, int &blk) {
+  const int seg = kb / a.kb_seg;
+  map = prob + seg;
+  blk = kb - seg * a.kb_seg;
+}
+
+// Loads this CTA's 128 A rows of K block blk (row0: first feature; E_GLU: 64
+// gate rows from ma[0], then 64 up rows from ma[1]).
+template <int EPI, int AMN, typename Load>
+PI_DEV void load_a(const Args &a, int map, int blk, int row0, uint32_t dst, Load load) {
+  constexpr int KE = EPI == E_I8 ? 128 : 64;  // elements of a K block
+  if constexpr (EPI == E_GLU) {
+    load(dst, &a.ma[0], blk * KE, row0);
+    load(dst + 8192, &a.ma[1], blk * KE, row0);
+  } else if constexpr (AMN) {
+    load(dst, &a.ma[map], row0, blk * 64);
+    load(dst + 8192, &a.ma[map], row0 + 64, blk * 64);
+  } else {
+    load(dst, &a.ma[map], blk * KE, row0);
+  }
+}
+
+// ================================================================ CTA-pair kernel
+constexpr int kPairThreads = 384;  // producer, MMA issuer, 2 idle warps, 8 epilogue warps
+constexpr int kPairEpi = 8;
+
+template <int NT>
+struct PairShape {
+  static constexpr int NB = NT / 2;            // B rows that one CTA of the pair loads
+  static constexpr int ABYTES = 16384;         // 128 rows x 128 bytes
+  static constexpr int STAGE = ABYTES + NB * 128;
+  static constexpr int NS = NT == 256 ? 6 : 8;
+  static constexpr int XCH_OFF = NS * STAGE;   // E_GLU: gate/up exchange, 4 warp pairs x 4 KB
+  static constexpr int CTRL_OFF = XCH_OFF + 16384;
+  static constexpr int SMEM = CTRL_OFF + 512 + 1024;  // + alignment slack
+  static constexpr uint32_t TMEM_COLS = 2 * NT;
+  static_assert(SMEM <= 227 * 1024, "shared memory");
+};
+
+template <int NS>
+struct Ctrl {
+  uint64_t full[NS], empty[NS], accfull[2], accfree[2];
+  uint32_t tmem;
+  int abort_flag;
+};
+
+struct TileAt {
+  int prob, m, n;  // tile indices
+};
+// Groups of 8 m tiles walked together over all n tiles: the tiles in flight
+// on the machine form a block of about 8 x 9, so each operand row is read
+// from HBM a few times and from L2 otherwise.
+PI_DEV TileAt tile_at(const Args &a, int t) {
+  constexpr int GM = 8;
+  const int per = a.mt * a.nt;
+  TileAt r;
+  r.prob = t / per;
+  const int rem = t - r.prob * per;
+  const int gsize = GM * a.nt;
+  const int g = rem / gsize, in = rem - g * gsize;
+  const int gm = min(GM, a.mt - g * GM);
+  r.n = in / gm;
+  r.m = g * GM + in - r.n * gm;
+  return r;
+}
+
+template <int EPI, int AMN, int BMN, int NT, typename T>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+    pair_gemm_kernel(const __grid_constant__ Args a) {
+  using S = PairShape<NT>;
+  constexpr bool I8 = EPI == E_I8;
+  constexpr int MROWS = EPI == E_GLU ? 64 : 128;  // features of one CTA's half tile
+  extern __shared__ unsigned char smem_raw[];
+  // the same offset in both CTAs of the pair (the dynamic shared window starts at the same place)
+  unsigned char *smem = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  using C_t = Ctrl<S::NS>;
+  static_assert(sizeof(C_t) <= 512, "control block");
+  C_t &C = *reinterpret_cast<C_t *>(smem + S::CTRL_OFF);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = (int)cluster_rank();
+  const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+  const int tiles = a.nprob * a.mt * a.nt;
+
+  if (tid == 0) {
+    for (int s = 0; s < S::NS; ++s) {
+      mbar_init(&C.full[s], 1);   // the leader's expect_tx; both CTAs' copies complete the bytes
+      mbar_init(&C.empty[s], 1);  // the leader's commit
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&C.accfull[b], 1);
+      mbar_init(&C.accfree[b], 2 * kPairEpi);  // the epilogue warps of both CTAs
+    }
+    C.abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 2) tmem_alloc_pair(&C.tmem, S::TMEM_COLS);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = C.tmem;
+  volatile int *abort_flag = &C.abort_flag;
+
+  pdl_wait();
+  pdl_launch_dependents();
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer (one lane)
+    if (lane == 0) {
+      long long it = 0;
+      bool ok = true;
+      for (int t = pair; t < tiles && ok; t += npairs) {
+        const TileAt at = tile_at(a, t);
+        const int row0 = (at.m * 2 + rank) * MROWS;
+        const int col0 = at.n * NT + rank * S::NB;
+        for (int kb = 0; kb < a.kb; ++kb, ++it) {
+          const int s = (int)(it % S::NS);
+          const unsigned ph = (unsigned)((it / S::NS) & 1);
+          if (it >= S::NS && !mbar_wait_cluster(&C.empty[s], ph ^ 1u, abort_flag, a.status)) {
+            ok = false;
+            break;
+          }
+          const uint32_t dst = su32(smem + s * S::STAGE);
+          const uint32_t bar = mapa(su32(&C.full[s]), 0);
+          if (rank == 0) mbar_expect_tx(&C.full[s], 2 * S::STAGE);
+          int map, blk;
+          k_at(a, at.prob, kb, map, blk);
+          load_a<EPI, AMN>(a, map, blk, row0, dst,
+                           [&](uint32_t d, const CUtensorMap *tm, int x, int y) { tma_load_2d_pair(d, tm, x, y, bar); });
+          const CUtensorMap *tb = &a.mb[map];
+          if constexpr (BMN) {
+#pragma unroll
+            for (int h = 0; h < S::NB / 64; ++h)
+              tma_load_2d_pair(dst + S::ABYTES + h * 8192, tb, col0 + h * 64, blk * 64, bar);
+          } else {
+            tma_load_2d_pair(dst + S::ABYTES, tb, blk * (I8 ? 128 : 64), col0, bar);
+          }
+        }
+      }
+      // the MMAs that read the last stages have finished before this CTA may go
+      for (long long j = it > S::NS ? it - S::NS : 0; j < it && ok; ++j)
+        ok = mbar_wait_cluster(&C.empty[j % S::NS], (unsigned)((j / S::NS) & 1), abort_flag, a.status);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer (one lane of the leader CTA)
+    if (rank == 0 && lane == 0) {
+      long long it = 0;
+      int tc = 0;
+      bool ok = true;
+      for (int t = pair; t < tiles && ok; t += npairs, ++tc) {
+        const int b = tc & 1;
+        if (tc >= 2 && !mbar_wait_cluster(&C.accfree[b], (unsigned)(((tc >> 1) & 1) ^ 1), abort_flag, a.status)) break;
+        tc_fence_after();
+        const uint32_t acc = tmem + (uint32_t)(b * NT);
+        for (int kb = 0; kb < a.kb; ++kb, ++it) {
+          const int s = (int)(it % S::NS);
+          if (!mbar_wait_cluster(&C.full[s], (unsigned)((it / S::NS) & 1), abort_flag, a.status)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t st = su32(smem + s * S::STAGE);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            mma<2, I8>(acc, operand_desc<AMN>(st, j), operand_desc<BMN>(st + S::ABYTES, j), a.idesc,
+                       (kb | j) ? 1u : 0u);
+          mma_commit_pair(&C.empty[s]);
+        }
+        if (ok) mma_commit_pair(&C.accfull[b]);
+      }
+    }
+    __syncwarp();
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------ epilogue: lane quarter q, column half h
+    const int q = warp & 3, h = (warp - 4) >> 2;
+    const int lrow = q * 32 + lane;  // row of this CTA's half tile
+    int tc = 0;
+    for (int t = pair; t < tiles; t += npairs, ++tc) {
+      const TileAt at = tile_at(a, t);
+      const int b = tc & 1;
+      bool ok = __all_sync(0xffffffffu, mbar_wait_cluster(&C.accfull[b], (unsigned)((tc >> 1) & 1), abort_flag, a.status));
+      if constexpr (EPI == E_GLU) {
+        // the exchange below needs all 8 warps: agree on going on
+        uint32_t bad;
+        asm volatile(
+            "{\n .reg .pred p, r;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred r, 1, 256, p;\n"
+            " selp.u32 %0, 1, 0, r;\n}\n"
+            : "=r"(bad)
+            : "r"(ok ? 0u : 1u)
+            : "memory");
+        ok = !bad;
+      }
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t tbase = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * NT + h * (NT / 2));
+      const int n0 = at.n * NT + h * (NT / 2);
+      if constexpr (EPI == E_GLU) {
+        // lanes 0..63 hold gate rows, lanes 64..127 the up rows of the same
+        // neurons: warps q and q + 2 swap half a chunk through shared memory
+        // and each finishes the other half
+        const int neuron = (at.m * 2 + rank) * 64 + (q & 1) * 32 + lane;
+        const bool in = neuron < a.m;
+        const bool is_up = q >= 2;
+        float *xb = reinterpret_cast<float *>(smem + S::XCH_OFF) + (h * 2 + (q & 1)) * 1024;
+        void *keep = is_up ? a.up_out : a.gate_out;
+#pragma unroll 1
+        for (int c = 0; c < NT / 32; ++c) {
+          float v[16];
+          tmem_ld16(tbase + c * 16, v);
+          float *buf = xb + (c & 1) * 512;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) buf[(is_up ? 256 : 0) + j * 32 + lane] = is_up ? v[j] : v[8 + j];
+          if (keep) put_t<16, T>(a, keep, neuron, n0 + c * 16, in, v);
+          asm volatile("bar.sync %0, 64;" ::"r"(2 + h * 2 + (q & 1)) : "memory");
+          float mine[8], other[8], o[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            mine[j] = is_up ? v[8 + j] : v[j];
+            other[j] = buf[(is_up ? 0 : 256) + j * 32 + lane];
+          }
+          if (is_up) glu<8>(a.act, other, mine, o);
+          else glu<8>(a.act, mine, other, o);
+          put_t<8, T>(a, a.out[0], neuron, n0 + c * 16 + (is_up ? 8 : 0), in, o);
+        }
+      } else {
+        const int m = (at.m * 2 + rank) * 128 + lrow;
+        const bool in = m < a.m;
+#pragma unroll 1
+        for (int c = 0; c < NT / 32; ++c) {
+          float v[16];
+          const int nc = n0 + c * 16;
+          if constexpr (EPI == E_DGLU) {
+            float g[16], p[16];
+            load_gp<16, T>(a, m, nc, in, g, p);
+            tmem_ld16(tbase + c * 16, v);
+            epi_dglu<16, T>(a, m, nc, in, v, g, p);
+          } else {
+            tmem_ld16(tbase + c * 16, v);
+            if constexpr (EPI == E_I8) epi_i8<16>(a, m, nc, in, v);
+            else put_cols<16>(a, a.out[at.prob], m, nc, in, v, a.out_type, a.accumulate);
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(mapa(su32(&C.accfree[b]), 0));
+    }
+  }
+  if (*abort_flag) __nanosleep(1000000);  // copies in flight land before the CTA goes
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  if (warp == 2) tmem_dealloc_pair(tmem, S::TMEM_COLS);
+}
+
+// ================================================================ split-K kernel
+constexpr int kSplitThreads = 192;  // producer, MMA issuer, 4 epilogue warps
+
+template <int NT>
+struct SplitShape {
+  static constexpr int ABYTES = 16384;
+  static constexpr int STAGE = ABYTES + NT * 128;
+  static constexpr int NS = NT <= 16 ? 6 : NT <= 32 ? 5 : NT <= 64 ? 4 : 3;  // two CTAs per SM
+  static constexpr int CTRL_OFF = NS * STAGE;
+  static constexpr int SMEM = CTRL_OFF + 512 + 1024;
+  static constexpr uint32_t TMEM_COLS = NT < 32 ? 32 : NT;
+  static_assert(NT * 512 <= NS * STAGE, "the partial tile fits the ring");
+  static_assert(2 * (SMEM + 1024) <= 228 * 1024, "two CTAs per SM");
+};
+
+template <int EPI, int AMN, int NT, typename T>
+__global__ void __launch_bounds__(kSplitThreads, 2) split_gemm_kernel(const __grid_constant__ Args a) {
+  using S = SplitShape<NT>;
+  constexpr bool I8 = EPI == E_I8;
+  constexpr int MROWS = EPI == E_GLU ? 64 : 128;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char *smem = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  using C_t = Ctrl<S::NS>;
+  C_t &C = *reinterpret_cast<C_t *>(smem + S::CTRL_OFF);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = (int)cluster_rank();
+  uint32_t csize;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(csize));
+  const int split = (int)csize;
+  const int tile = blockIdx.x / split;
+  const int mtile = tile % a.mt, ntile = tile / a.mt;
+  const int row0 = mtile * MROWS, col0 = ntile * NT;
+  const int k0 = (int)((long long)a.kb * rank / split), k1 = (int)((long long)a.kb * (rank + 1) / split);
+
+  if (tid == 0) {
+    for (int s = 0; s < S::NS; ++s) {
+      mbar_init(&C.full[s], 1);
+      mbar_init(&C.empty[s], 1);
+    }
+    mbar_init(&C.accfull[0], 1);
+    C.abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) tmem_alloc(&C.tmem, S::TMEM_COLS);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = C.tmem;
+  volatile int *abort_flag = &C.abort_flag;
+  bool fine = true;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer (one lane)
+    if (lane == 0) {
+      auto start_a = [&](int kb, int s) {
+        int map, blk;
+        k_at(a, 0, kb, map, blk);
+        mbar_expect_tx(&C.full[s], S::STAGE);
+        load_a<EPI, AMN>(a, map, blk, row0, su32(smem + s * S::STAGE),
+                         [&](uint32_t d, const CUtensorMap *tm, int x, int y) { tma_load_2d(d, tm, x, y, &C.full[s]); });
+      };
+      // the first stages' weights do not depend on the previous kernel of the same call
+      const int early = a.early_a ? min(S::NS, k1 - k0) : 0;
+      for (int i = 0; i < early; ++i) start_a(k0 + i, i);
+      pdl_wait();
+      for (int kb = k0; kb < k1; ++kb) {
+        const int i = kb - k0, s = i % S::NS;
+        const unsigned ph = (unsigned)((i / S::NS) & 1);
+        if (i >= S::NS && !mbar_wait(&C.empty[s], ph ^ 1u, abort_flag, a.status)) break;
+        if (i >= early) start_a(kb, s);
+        int map, blk;
+        k_at(a, 0, kb, map, blk);
+        tma_load_2d(su32(smem + s * S::STAGE + S::ABYTES), &a.mb[map], blk * (I8 ? 128 : 64), col0, &C.full[s]);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer (one lane)
+    if (lane == 0) {
+      bool ok = true;
+      for (int kb = k0; kb < k1; ++kb) {
+        const int i = kb - k0, s = i % S::NS;
+        if (!mbar_wait(&C.full[s], (unsigned)((i / S::NS) & 1), abort_flag, a.status)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t st = su32(smem + s * S::STAGE);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          mma<1, I8>(tmem, operand_desc<AMN>(st, j), operand_desc<0>(st + S::ABYTES, j), a.idesc, (i | j) ? 1u : 0u);
+        mma_commit(&C.empty[s]);
+      }
+      if (ok) mma_commit(&C.accfull[0]);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ partial tile to shared memory
+    const int q = warp & 3;
+    float *red = reinterpret_cast<float *>(smem);
+    fine = mbar_wait_warp(&C.accfull[0], 0u, abort_flag, a.status);
+    if (fine) {
+      tc_fence_after();
+      const int nv = min(NT, a.n - col0);
+#pragma unroll
+      for (int c = 0; c < NT / 16; ++c) {
+        if (c * 16 < nv) {  // the same for the whole warp
+          float v[16];
+          tmem_ld16(tmem + ((uint32_t)(q * 32) << 16) + c * 16, v);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) red[(c * 16 + j) * 128 + q * 32 + lane] = v[j];
+        }
+      }
+    }
+  }
+  if (*abort_flag) __nanosleep(1000000);  // copies in flight land before the CTA goes
+  pdl_wait();
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // every CTA's partial tile is in its shared memory
+  pdl_launch_dependents();
+  {
+    // ------------------------------------------------------------ join: this CTA's slice of the tile, summed in rank order
+    const int nv = min(NT, a.n - col0);
+    const int E = nv * MROWS;
+    const int per = ((E + split * 32 - 1) / (split * 32)) * 32;
+    const int e0 = rank * per, e1 = min(E, e0 + per);
+    const uint32_t red = su32(smem);
+    for (int e = e0 + tid; e < e1; e += kSplitThreads) {
+      const int n = e / MROWS, r = e % MROWS;
+      const uint32_t off = red + (uint32_t)(n * 128 + r) * 4;
+      const int m = row0 + r;
+      const bool in = m < a.m;
+      float v[1], w[1] = {0.f};
+      if constexpr (I8) {
+        int sum = 0;
+#pragma unroll 4
+        for (int c = 0; c < split; ++c) sum += __float_as_int(ld_cluster_f32(mapa(off, c)));
+        v[0] = __int_as_float(sum);
+        epi_i8<1>(a, m, col0 + n, in, v);
+      } else {
+        v[0] = 0.f;
+#pragma unroll 4
+        for (int c = 0; c < split; ++c) {
+          v[0] += ld_cluster_f32(mapa(off, c));
+          if constexpr (EPI == E_GLU) w[0] += ld_cluster_f32(mapa(off + 256, c));
+        }
+        if constexpr (EPI == E_GLU) {
+          float o[1];
+          glu<1>(a.act, v, w, o);
+          if (a.gate_out) put_t<1, T>(a, a.gate_out, m, col0 + n, in, v);
+          if (a.up_out) put_t<1, T>(a, a.up_out, m, col0 + n, in, w);
+          put_t<1, T>(a, a.out[0], m, col0 + n, in, o);
+        } else if constexpr (EPI == E_DGLU) {
+          float g[1], p[1];
+          load_gp<1, T>(a, m, col0 + n, in, g, p);
+          epi_dglu<1, T>(a, m, col0 + n, in, v, g, p);
+        } else {
+          put_cols<1>(a, a.out[0], m, col0 + n, in, v, a.out_type, a.accumulate);
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  cluster_sync();  // the others have read this CTA's partial tile
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, S::TMEM_COLS);
+}
+
+}  // namespace gemm
+}  // namespace pi

@@ -228,6 +228,124 @@ pi_status pi_decode_ffn_static(pi_ffn_t h, const void *u, float *y, int32_t *idx
  * call is running. */
 pi_status pi_debug_wait_fault(int withhold_row, unsigned limit_us);
 
+/* ====================================================================
+ * Dense block operators: the same FFN block over ALL its neurons for any
+ * number of tokens (prompts, training), the norms and residual add around a
+ * block, and an 8-bit integer product for serving.  The pages have no
+ * counterpart; they complete the block whose sparse decode step is above.
+ *
+ * Conventions: those at the top of this file, and
+ *  - every tensor is contiguous and 16-byte aligned; token counts may be 0
+ *    (per-token pointers may then be NULL, nothing is read, and gradients that
+ *    sum over tokens are set to zero) and are at most 2^24; outputs overlap no
+ *    input and no other output unless stated;
+ *  - products accumulate in fp32 (int32 for 8-bit codes), and norms, gates
+ *    and their statistics are fp32; a value is rounded where it is stored;
+ *  - results do not depend on timing: every sum has a fixed order;
+ *  - non-finite inputs give non-finite results in the rows (for gradients of
+ *    weights, the columns) that they enter, and touch no others;
+ *  - a workspace's first 256 bytes must be zero before its first use
+ *    (pi_workspace_init, or any memset of them); it belongs to one call at a
+ *    time.  The bounded waits of these kernels report PI_ERR_TIMEOUT through
+ *    pi_get_device_status(ws). */
+typedef enum pi_dtype { PI_DT_F32 = 0, PI_DT_F16 = 1, PI_DT_BF16 = 2 } pi_dtype;
+
+/* phi(g): SiLU g / (1 + e^-g); ReLU max(g, 0), slope 0 at 0; GELU
+ * g (1 + erf(g / sqrt 2)) / 2. */
+typedef enum pi_gate_act { PI_GATE_SILU = 0, PI_GATE_RELU = 1, PI_GATE_GELU = 2 } pi_gate_act;
+
+enum { PI_GRAD_ACCUMULATE = 1u /* parameter gradients are added to their outputs */ };
+
+/* Gated feed-forward block: g = Wg u, p = Wu u, a = phi(g) p,
+ * y = sum_i a_i W2T_i.  Weights [f x d], neuron-major like the sparse path's;
+ * device memory, borrowed while the handle is used (their values may change
+ * between calls, as in training). */
+typedef struct pi_gated_ffn_desc {
+  int d_model, d_ffn; /* multiples of 8, at most 2^20 */
+  int act;            /* pi_gate_act */
+  int dtype;          /* pi_dtype of weights, u, y, g, p: PI_DT_F16 or PI_DT_BF16 */
+  const void *w_gate, *w_up, *w_down_t;
+} pi_gated_ffn_desc;
+
+typedef struct pi_gated_ffn *pi_gated_ffn_t; /* host-side handle; holds no device memory */
+
+pi_status pi_gated_ffn_create(const pi_gated_ffn_desc *desc, pi_gated_ffn_t *out);
+void pi_gated_ffn_destroy(pi_gated_ffn_t h);
+
+/* Workspace bytes for calls of up to max_tokens tokens: the activations a
+ * (and, with backward != 0, the gradients of g and p), 16-bit [tokens x f]. */
+pi_status pi_gated_ffn_workspace_size(pi_gated_ffn_t h, int max_tokens, int backward, size_t *bytes);
+
+/* y [tokens x d] from u [tokens x d].  gate, up: optional outputs
+ * [tokens x f], the pre-activations g and p rounded to the layer's type, which
+ * the backward pass takes.  a is rounded to the layer's type once, from fp32
+ * g and p, on its way to the second product. */
+pi_status pi_gated_ffn_forward(pi_gated_ffn_t h, const void *u, int tokens, void *y, void *gate, void *up, void *ws,
+                               size_t ws_bytes, pi_stream_t stream);
+
+/* Gradients for dy [tokens x d], at the u, gate and up of a forward call:
+ *   da = dy W2T^T, dg = da p phi'(g), dp = da phi(g),
+ *   du = dg Wg + dp Wu,  dWg = dg^T u, dWu = dp^T u, dW2T = (phi(g) p)^T dy.
+ * du [tokens x d] in the layer's type; dw_* [f x d] in grad_dtype (fp32 or the
+ * layer's type).  Each output may be NULL.  dg, dp and a enter the products
+ * rounded to the layer's type.  flags: PI_GRAD_ACCUMULATE (dw_* only). */
+pi_status pi_gated_ffn_backward(pi_gated_ffn_t h, const void *u, const void *gate, const void *up, const void *dy,
+                                int tokens, void *du, void *dw_gate, void *dw_up, void *dw_down_t, int grad_dtype,
+                                unsigned flags, void *ws, size_t ws_bytes, pi_stream_t stream);
+
+/* Norms before and after a block, with its gate and residual scale.  For the
+ * residual stream x and a block's output y, per token:
+ *   b = w_post y / sqrt(mean(y^2) + eps)   (post_norm; otherwise b = y)
+ *   r = residual_scale x + branch_scale gate b      (the new stream)
+ *   u = w_pre r / sqrt(mean(r^2) + eps)             (the next block's input)
+ * Token t uses gate row t / tokens_per_gate: one row for all tokens, one per
+ * sequence, or one per token. */
+typedef struct pi_block_norm_desc {
+  int d_model;           /* a multiple of 8, at most 16384 */
+  int y_dtype, u_dtype;  /* pi_dtype of y and u (any); x, r and parameters are fp32 */
+  int post_norm;         /* normalise y */
+  float eps;             /* > 0 */
+  float residual_scale, branch_scale;
+  const float *w_post, *w_pre; /* [d] or NULL (ones); w_post needs post_norm */
+  const float *gate;     /* [ceil(tokens / tokens_per_gate) x d] or NULL (ones) */
+  int tokens_per_gate;   /* > 0 with a gate; else ignored */
+} pi_block_norm_desc;
+
+/* x [tokens x d] -> x_out (r; may be x itself) and u, at least one of them.
+ * y may be NULL: r = residual_scale x.  rstd_post, rstd_pre: optional outputs
+ * [tokens], the factors 1 / sqrt(mean + eps), which the backward pass takes. */
+pi_status pi_block_norm_forward(const pi_block_norm_desc *desc, const float *x, const void *y, int tokens,
+                                float *x_out, void *u, float *rstd_post, float *rstd_pre, pi_stream_t stream);
+
+pi_status pi_block_norm_workspace_size(const pi_block_norm_desc *desc, int max_tokens, size_t *bytes);
+
+/* Gradients at a forward call's x_out, y and factors, for du (NULL: u is not
+ * used) and dx_out, the gradient that reaches the new stream by other ways
+ * (NULL: none); at least one of the two.  dx [tokens x d] fp32 (may be dx_out
+ * itself), dy [tokens x d] in y_dtype (may be y itself), dw_post, dw_pre [d] and
+ * dgate (the gate's shape) fp32; each may be NULL.  flags: PI_GRAD_ACCUMULATE
+ * (dw_post, dw_pre, dgate). */
+pi_status pi_block_norm_backward(const pi_block_norm_desc *desc, const float *x_out, const void *y,
+                                 const float *rstd_post, const float *rstd_pre, const void *du, const float *dx_out,
+                                 int tokens, float *dx, void *dy, float *dw_post, float *dw_pre, float *dgate,
+                                 unsigned flags, void *ws, size_t ws_bytes, pi_stream_t stream);
+
+/* 8-bit codes of each row of x [rows x k] (tokens, or the output channels of
+ * a weight; x_dtype: pi_dtype; k a multiple of 16, at most 131056):
+ *   scale = max |x| / 127,  q = x / scale rounded to the nearest integer,
+ * with an fp32 scale and quotient, ties to even.  A row of zeros has scale 0;
+ * a row with an infinity or a NaN has scale NaN and codes 0. */
+pi_status pi_quantize_i8(const void *x, int x_dtype, int rows, int k, int8_t *q, float *scales, pi_stream_t stream);
+
+pi_status pi_matmul_i8_workspace_size(int tokens, int n, int k, size_t *bytes);
+
+/* y[t, c] = x_scales[t] w_scales[c] sum_k xq[t, k] wq[c, k] + bias[c]
+ * for xq [tokens x k], wq [n x k], any n; exact int32 sums (codes -128..127).
+ * y [tokens x n] in y_dtype (any pi_dtype); bias [n] fp32 or NULL. */
+pi_status pi_matmul_i8(const int8_t *xq, const float *x_scales, const int8_t *wq, const float *w_scales,
+                       const float *bias, int tokens, int n, int k, void *y, int y_dtype, void *ws, size_t ws_bytes,
+                       pi_stream_t stream);
+
 /* Synchronise the stream, read and clear the workspace status word.  *code is
  * PI_OK or the first device-side error recorded since the last read. */
 pi_status pi_get_device_status(void *ws, pi_stream_t stream, int *code);
