@@ -74,13 +74,13 @@ cudaError_t launch1(void (*kern)(KArg), dim3 grid, int threads, size_t smem, int
   return cudaLaunchKernelEx(&cfg, kern, arg);
 }
 
-template <int EPI, int AMN, int BMN, int NT, typename T>
+template <int EPI, int AMN, int BMN, int MB, int NT, typename T>
 cudaError_t pair_launch(const GM::Args &a, int sms, cudaStream_t st) {
   static DeviceOnce once;
   const long long tiles = (long long)a.nprob * a.mt * a.nt;
   const int pairs = (int)(tiles < sms / 2 ? tiles : sms / 2);
-  return launch1(GM::pair_gemm_kernel<EPI, AMN, BMN, NT, T>, dim3(2 * pairs), GM::kPairThreads,
-                 GM::PairShape<NT>::SMEM, 0, &once, st, a);
+  return launch1(GM::pair_gemm_kernel<EPI, AMN, BMN, MB, NT, T>, dim3(2 * pairs), GM::kPairThreads,
+                 GM::PairShape<EPI, MB, NT>::SMEM, 0, &once, st, a);
 }
 template <int EPI, int AMN, int NT, typename T>
 cudaError_t split_launch(const GM::Args &a, int split, cudaStream_t st) {
@@ -89,16 +89,27 @@ cudaError_t split_launch(const GM::Args &a, int split, cudaStream_t st) {
                  GM::SplitShape<NT>::SMEM, split, &once, st, a);
 }
 
-// How a product runs.  nt: token columns of a tile; split: 0 = CTA-pair
-// kernel, else the cluster size that K is split over.
+// How a product runs.  nt: token columns of a tile; mb: 256-feature blocks of
+// a CTA-pair tile; split: 0 = CTA-pair kernel, else the cluster size that K is
+// split over.
 struct Plan {
-  int nt, split;
+  int nt, mb, split;
   int b_rows() const { return split ? nt : nt / 2; }  // rows of the B box
 };
 
-// m_rows: features of a 128-row tile (64 for the gate | up product).
-Plan choose(int m, int m_rows, int n, int kb, int sms) {
+// Time of a CTA-pair tiling, in SM cycles: rounds of tiles x K blocks x the
+// slower of the MMAs (2 cycles a column and block) and the stage's bytes at
+// the L2's rate per SM, plus the epilogue that no MMA covers.
+double pair_cost(long long tiles, int pairs, int kb, int mb, int nt) {
+  const double mma = 2.0 * mb * nt, load = (mb * 16384 + nt * 64) / 42.0;
+  return (double)((tiles + pairs - 1) / pairs) * (kb * (mma > load ? mma : load) + (mb == 2 ? 3000.0 : 1000.0));
+}
+
+// m_rows: features of a 128-row tile (64 for the gate | up product).  max_mb,
+// nt192: the tilings built for this product.
+Plan choose(int m, int m_rows, int n, int kb, int sms, int max_mb, bool nt192) {
   Plan p{};
+  p.mb = 1;
   auto split_of = [&](int tiles) {
     int s = 1;
     while (s < 8 && tiles * s < sms && kb >= 4 * s) s *= 2;
@@ -117,9 +128,13 @@ Plan choose(int m, int m_rows, int n, int kb, int sms) {
     p.split = split_of(mt * cdiv(n, 128));
     return p;
   }
-  const auto waves = [&](int nt) { return (long long)cdiv(cdiv(m, 2 * m_rows) * cdiv(n, nt), pairs) * (nt + 32); };
-  p.nt = waves(128) < waves(256) ? 128 : 256;
-  p.split = 0;
+  double best = 0;
+  for (int mb = 1; mb <= max_mb; ++mb)
+    for (int nt = 128; nt <= 256; nt += 64) {
+      if (nt == 192 ? !nt192 || mb != 2 : nt == 128 && mb == 2) continue;
+      const double c = pair_cost((long long)cdiv(m, 2 * mb * m_rows) * cdiv(n, nt), pairs, kb, mb, nt);
+      if (best == 0 || c < best) best = c, p.mb = mb, p.nt = nt;
+    }
   return p;
 }
 
@@ -131,11 +146,19 @@ uint32_t idesc(int dtype, bool i8, int M, int N, int a_mn, int b_mn) {
 
 template <int EPI, int AMN, typename T>
 cudaError_t run_plan(GM::Args &a, const Plan &p, int dtype, int m_rows, int sms, cudaStream_t st) {
-  a.mt = cdiv(a.m, p.split ? m_rows : 2 * m_rows);
+  a.mt = cdiv(a.m, p.split ? m_rows : 2 * p.mb * m_rows);
   a.nt = cdiv(a.n, p.nt);
   a.idesc = idesc(dtype, EPI == GM::E_I8, p.split ? 128 : 256, p.nt, AMN, 0);
-  if (!p.split)
-    return p.nt == 256 ? pair_launch<EPI, AMN, 0, 256, T>(a, sms, st) : pair_launch<EPI, AMN, 0, 128, T>(a, sms, st);
+  if (!p.split) {
+    if constexpr (EPI != GM::E_DGLU) {
+      if (p.mb == 2 && p.nt == 256) return pair_launch<EPI, AMN, 0, 2, 256, T>(a, sms, st);
+    }
+    if constexpr (EPI == GM::E_STORE || EPI == GM::E_I8) {
+      if (p.mb == 2) return pair_launch<EPI, AMN, 0, 2, 192, T>(a, sms, st);
+    }
+    return p.nt == 256 ? pair_launch<EPI, AMN, 0, 1, 256, T>(a, sms, st)
+                       : pair_launch<EPI, AMN, 0, 1, 128, T>(a, sms, st);
+  }
   switch (p.nt) {
   case 16:
     return split_launch<EPI, AMN, 16, T>(a, p.split, st);
@@ -182,7 +205,7 @@ pi_status ffn_forward(const pi_gated_ffn *h, const void *u, int tokens, void *y,
     GM::Args a{};
     a.m = f, a.n = tokens, a.nprob = 1;
     a.kb = a.kb_seg = cdiv(d, 64);
-    const Plan p = choose(f, 64, tokens, a.kb, sms);
+    const Plan p = choose(f, 64, tokens, a.kb, sms, 2, false);
     a.ma[0] = h->gate64, a.ma[1] = h->up64;
     if (!map16(&a.mb[0], u, tokens, d, p.b_rows())) return PI_ERR_CUDA;
     a.out[0] = w.a;
@@ -195,7 +218,7 @@ pi_status ffn_forward(const pi_gated_ffn *h, const void *u, int tokens, void *y,
   GM::Args a{};
   a.m = d, a.n = tokens, a.nprob = 1;
   a.kb = a.kb_seg = cdiv(f, 64);
-  const Plan p = choose(d, 128, tokens, a.kb, sms);
+  const Plan p = choose(d, 128, tokens, a.kb, sms, 2, true);
   a.ma[0] = h->down64;
   if (!map16(&a.mb[0], w.a, tokens, f, p.b_rows())) return PI_ERR_CUDA;
   a.out[0] = y;
@@ -219,9 +242,12 @@ pi_status ffn_backward(const pi_gated_ffn *h, const void *u, const void *gate, c
     GM::Args a{};
     a.m = f, a.n = tokens, a.nprob = 1;
     a.kb = a.kb_seg = cdiv(d, 64);
-    const Plan p = choose(f, 128, tokens, a.kb, sms);
+    const Plan p = choose(f, 128, tokens, a.kb, sms, 1, false);
     a.ma[0] = h->down128;
     if (!map16(&a.mb[0], dy, tokens, d, p.b_rows())) return PI_ERR_CUDA;
+    if (!p.split && (!map_2d(&a.ma[1], gate, true, (uint64_t)f, (uint64_t)tokens, 128, (uint32_t)p.nt, false) ||
+                     !map_2d(&a.ma[2], up, true, (uint64_t)f, (uint64_t)tokens, 128, (uint32_t)p.nt, false)))
+      return PI_ERR_CUDA;
     a.out[0] = w.a;
     a.ldo = f;
     a.act = h->d.act;
@@ -253,10 +279,15 @@ pi_status ffn_backward(const pi_gated_ffn *h, const void *u, const void *gate, c
       a.out_type = grad_dtype;
       a.accumulate = acc;
       a.status = w.status;
-      a.mt = cdiv(d, 256);
+      const int mb = pair_cost((long long)a.nprob * cdiv(d, 512) * cdiv(f, 256), sms / 2, a.kb, 2, 256) <
+                             pair_cost((long long)a.nprob * cdiv(d, 256) * cdiv(f, 256), sms / 2, a.kb, 1, 256)
+                         ? 2
+                         : 1;
+      a.mt = cdiv(d, 256 * mb);
       a.nt = cdiv(f, 256);
       a.idesc = idesc(dt, false, 256, 256, 1, 1);
-      PI_TRY((pair_launch<GM::E_STORE, 1, 1, 256, T>(a, sms, st)));
+      PI_TRY((mb == 2 ? pair_launch<GM::E_STORE, 1, 1, 2, 256, T>(a, sms, st)
+                      : pair_launch<GM::E_STORE, 1, 1, 1, 256, T>(a, sms, st)));
     }
   }
   if (du) {
@@ -265,7 +296,7 @@ pi_status ffn_backward(const pi_gated_ffn *h, const void *u, const void *gate, c
     a.m = d, a.n = tokens, a.nprob = 1;
     a.kb_seg = cdiv(f, 64);
     a.kb = 2 * a.kb_seg;
-    const Plan p = choose(d, 128, tokens, a.kb, sms);
+    const Plan p = choose(d, 128, tokens, a.kb, sms, 2, true);
     a.ma[0] = h->gate64, a.ma[1] = h->up64;
     if (!map16(&a.mb[0], w.dg, tokens, f, p.b_rows()) || !map16(&a.mb[1], w.dp, tokens, f, p.b_rows()))
       return PI_ERR_CUDA;
@@ -575,7 +606,7 @@ pi_status pi_matmul_i8(const int8_t *xq, const float *x_scales, const int8_t *wq
   GM::Args a{};
   a.m = n, a.n = tokens, a.nprob = 1;
   a.kb = a.kb_seg = cdiv(k, 128);
-  const Plan p = choose(n, 128, tokens, a.kb, sms);
+  const Plan p = choose(n, 128, tokens, a.kb, sms, 2, true);
   if (!map_2d(&a.ma[0], wq, false, (uint64_t)k, (uint64_t)n, 128, 128, true) ||
       !map_2d(&a.mb[0], xq, false, (uint64_t)k, (uint64_t)tokens, 128, (uint32_t)p.b_rows(), true))
     return PI_ERR_CUDA;

@@ -50,7 +50,7 @@ enum OutType { O_F32 = 0, O_F16 = 1, O_BF16 = 2 };
 constexpr int kMaxMaps = 3;
 
 struct Args {
-  CUtensorMap ma[kMaxMaps], mb[kMaxMaps];  // operand maps, by problem or by K segment
+  CUtensorMap ma[kMaxMaps], mb[kMaxMaps];  // operand maps, by problem or by K segment (E_DGLU: ma[1], ma[2] of g, p)
   int m, n;          // extents (E_GLU: m = neurons)
   int kb, kb_seg;    // K blocks per tile; per segment (kb = kb_seg x segments)
   int nprob;         // independent products of the same shape (1 segment each)
@@ -130,8 +130,11 @@ PI_DEV void tma_load_2d_pair(uint32_t dst, const CUtensorMap *tm, int x, int y, 
       "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(bar)
       : "memory");
 }
-PI_DEV void prefetch_map(const CUtensorMap *tm) {
-  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(tm)) : "memory");
+// the box at (x, y) into L2 (no shared memory, no completion)
+PI_DEV void prefetch_l2_2d(const CUtensorMap *tm, int x, int y) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(tm)),
+               "r"(x), "r"(y)
+               : "memory");
 }
 
 template <int GROUP, bool I8>
@@ -197,17 +200,18 @@ template <> struct Elem<__nv_bfloat16> {
 };
 
 // ---------------------------------------------------------------- gate activations
-// phi and phi' in fp32; the caller rounds once.
+// phi and phi' in fp32; the caller rounds once.  The approximate exponential
+// and quotient (about 2^-21 relative) stay far below that rounding.
 template <int ACT>
 PI_DEV float gate_phi(float g) {
-  if constexpr (ACT == G_SILU) return g / (1.f + __expf(-g));
+  if constexpr (ACT == G_SILU) return __fdividef(g, 1.f + __expf(-g));
   if constexpr (ACT == G_RELU) return g < 0.f ? 0.f : g;  // NaN stays NaN
   return 0.5f * g * (1.f + erff(g * 0.70710678f));
 }
 template <int ACT>
 PI_DEV void gate_phi_grad(float g, float &phi, float &slope) {
   if constexpr (ACT == G_SILU) {
-    const float s = 1.f / (1.f + __expf(-g));
+    const float s = __fdividef(1.f, 1.f + __expf(-g));
     phi = g * s;
     slope = s * (1.f + g * (1.f - s));
   } else if constexpr (ACT == G_RELU) {
@@ -221,43 +225,94 @@ PI_DEV void gate_phi_grad(float g, float &phi, float &slope) {
 }
 
 // ---------------------------------------------------------------- element epilogues
-// NC consecutive columns n0.. of feature m; `ok` is m < a.m.  vals: fp32 sums
-// (E_I8: int32 bits).
-template <int NC>
-PI_DEV void put_cols(const Args &a, void *out, int m, int n0, bool ok, const float (&v)[NC], int type, int acc) {
-  if (!ok) return;
-  const size_t at = (size_t)n0 * a.ldo + m;
-  if (type == O_F32) {
-    float *p = reinterpret_cast<float *>(out) + at;
-#pragma unroll
-    for (int j = 0; j < NC; ++j)
-      if (n0 + j < a.n) p[(size_t)j * a.ldo] = acc ? p[(size_t)j * a.ldo] + v[j] : v[j];
-  } else if (type == O_F16) {
-    __half *p = reinterpret_cast<__half *>(out) + at;
-#pragma unroll
-    for (int j = 0; j < NC; ++j)
-      if (n0 + j < a.n) {
-        __half *q = p + (size_t)j * a.ldo;
-        *q = __float2half_rn(acc ? __half2float(*q) + v[j] : v[j]);
-      }
+// NC consecutive columns n0.. of feature m (the lane's row); E_I8 sums are
+// int32 bits.  `ok` is m < a.m.  Whole 32-feature, NC-column pieces of 16-bit
+// matrices move as 4-byte words of two features: a lane pair swaps halves, so
+// that the even lane holds both features of an even column and the odd lane
+// those of the next column.  That costs 3 instructions an element where the
+// guarded scalar form costs about 24, which the CTA-pair kernel's single
+// accumulator set (MB = 2) would expose: 68% tensor-pipe activity against 86%
+// (dW of 4096 x 5120 x 5120).
+template <typename T>
+PI_DEV uint32_t pack2(float lo, float hi) {
+  if constexpr (sizeof(T) == 2 && __is_same(T, __half)) {
+    const __half2 w = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&w);
   } else {
-    __nv_bfloat16 *p = reinterpret_cast<__nv_bfloat16 *>(out) + at;
-#pragma unroll
-    for (int j = 0; j < NC; ++j)
-      if (n0 + j < a.n) {
-        __nv_bfloat16 *q = p + (size_t)j * a.ldo;
-        *q = __float2bfloat16_rn(acc ? __bfloat162float(*q) + v[j] : v[j]);
-      }
+    const __nv_bfloat162 w = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&w);
   }
+}
+template <typename T>
+PI_DEV void unpack2(uint32_t w, float &lo, float &hi) {
+  if constexpr (__is_same(T, __half)) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w));
+    lo = f.x, hi = f.y;
+  } else {
+    lo = __uint_as_float(w << 16), hi = __uint_as_float(w & 0xffff0000u);
+  }
+}
+// (column j, column j + 1) of one feature <-> (even feature, odd feature) of column j + (lane & 1)
+PI_DEV uint32_t pair_swap(uint32_t w) {
+  const uint32_t r = __shfl_xor_sync(0xffffffffu, w, 1);
+  return __byte_perm(w, r, (threadIdx.x & 1) ? 0x3276 : 0x5410);
+}
+// the warp's 32 features and NC columns lie inside the matrix, and words of two features are aligned
+template <int NC>
+PI_DEV bool whole_piece(const Args &a, int m, int n0) {
+  return (m | 31) < a.m && n0 + NC <= a.n && (a.ldo & 1) == 0;
 }
 
 template <int NC, typename T>
 PI_DEV void put_t(const Args &a, void *out, int m, int n0, bool ok, const float (&v)[NC]) {
+  if constexpr (NC % 2 == 0) {
+    if (whole_piece<NC>(a, m, n0)) {
+      char *p = reinterpret_cast<char *>(reinterpret_cast<T *>(out) + (size_t)(n0 + (threadIdx.x & 1)) * a.ldo + (m & ~1));
+      const long long step = 4 * a.ldo;
+#pragma unroll
+      for (int j = 0; j < NC; j += 2, p += step) *reinterpret_cast<uint32_t *>(p) = pair_swap(pack2<T>(v[j], v[j + 1]));
+      return;
+    }
+  }
   if (!ok) return;
   T *p = reinterpret_cast<T *>(out) + (size_t)n0 * a.ldo + m;
 #pragma unroll
   for (int j = 0; j < NC; ++j)
     if (n0 + j < a.n) p[(size_t)j * a.ldo] = Elem<T>::from(v[j]);
+}
+template <int NC>
+PI_DEV void put_f32(const Args &a, void *out, int m, int n0, bool ok, const float (&v)[NC]) {
+  if (!ok) return;
+  float *p = reinterpret_cast<float *>(out) + (size_t)n0 * a.ldo + m;
+  if (n0 + NC <= a.n) {
+#pragma unroll
+    for (int j = 0; j < NC; ++j, p += a.ldo) *p = v[j];
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < NC; ++j)
+    if (n0 + j < a.n) p[(size_t)j * a.ldo] = v[j];
+}
+template <int NC, typename T>
+PI_DEV void add_t(const Args &a, const void *out, int m, int n0, bool ok, float (&v)[NC]) {
+  const T *p = reinterpret_cast<const T *>(out) + (size_t)n0 * a.ldo + m;
+#pragma unroll
+  for (int j = 0; j < NC; ++j)
+    if (ok && n0 + j < a.n) {
+      if constexpr (__is_same(T, float)) v[j] += p[(size_t)j * a.ldo];
+      else v[j] += Elem<T>::to(p[(size_t)j * a.ldo]);
+    }
+}
+// out: fp32 or T; acc: what is there is added first, and the sum is rounded once
+template <int NC, typename T>
+PI_DEV void put_cols(const Args &a, void *out, int m, int n0, bool ok, float (&v)[NC], int type, int acc) {
+  if (type == O_F32) {
+    if (acc) add_t<NC, float>(a, out, m, n0, ok, v);
+    put_f32<NC>(a, out, m, n0, ok, v);
+  } else {
+    if (acc) add_t<NC, T>(a, out, m, n0, ok, v);
+    put_t<NC, T>(a, out, m, n0, ok, v);
+  }
 }
 
 template <int NC>
@@ -267,10 +322,12 @@ PI_DEV void epi_i8(const Args &a, int m, int n0, bool ok, const float (&v)[NC]) 
   float o[NC];
 #pragma unroll
   for (int j = 0; j < NC; ++j) {
-    const float sn = n0 + j < a.n ? __ldg(a.s_n + n0 + j) : 0.f;
+    const float sn = __ldg(a.s_n + min(n0 + j, a.n - 1));
     o[j] = fmaf((float)__float_as_int(v[j]) * sn, sm, b);
   }
-  put_cols<NC>(a, a.out[0], m, n0, ok, o, a.out_type, 0);
+  if (a.out_type == O_F32) put_f32<NC>(a, a.out[0], m, n0, ok, o);
+  else if (a.out_type == O_F16) put_t<NC, __half>(a, a.out[0], m, n0, ok, o);
+  else put_t<NC, __nv_bfloat16>(a, a.out[0], m, n0, ok, o);
 }
 
 template <int NC, typename T, int ACT>
@@ -289,15 +346,43 @@ PI_DEV void epi_dglu_act(const Args &a, int m, int n0, bool ok, const float (&v)
   put_t<NC, T>(a, a.up_out, m, n0, ok, dp);
   put_t<NC, T>(a, a.out[0], m, n0, ok, av);
 }
+// NC columns of a 16-bit matrix, as words of two columns of this lane's feature; zero outside
+template <int NC, typename T>
+PI_DEV void load_pairs(const Args &a, const void *in, int m, int n0, bool ok, uint32_t (&w)[(NC + 1) / 2]) {
+  if constexpr (NC % 2 == 0) {
+    if (whole_piece<NC>(a, m, n0)) {
+      const char *p = reinterpret_cast<const char *>(reinterpret_cast<const T *>(in) +
+                                                     (size_t)(n0 + (threadIdx.x & 1)) * a.ldo + (m & ~1));
+      const long long step = 4 * a.ldo;
+#pragma unroll
+      for (int j = 0; j < NC / 2; ++j, p += step) w[j] = *reinterpret_cast<const uint32_t *>(p);
+#pragma unroll
+      for (int j = 0; j < NC / 2; ++j) w[j] = pair_swap(w[j]);
+      return;
+    }
+  }
+  const uint16_t *p = reinterpret_cast<const uint16_t *>(in) + (size_t)n0 * a.ldo + m;
+#pragma unroll
+  for (int j = 0; j < NC; j += 2) {
+    const uint32_t lo = ok && n0 + j < a.n ? p[(size_t)j * a.ldo] : 0u;
+    const uint32_t hi = j + 1 < NC && ok && n0 + j + 1 < a.n ? p[(size_t)(j + 1) * a.ldo] : 0u;
+    w[j / 2] = lo | hi << 16;
+  }
+}
 template <int NC, typename T>
 PI_DEV void load_gp(const Args &a, int m, int n0, bool ok, float (&g)[NC], float (&p)[NC]) {
-  const T *gi = reinterpret_cast<const T *>(a.gate_in) + (size_t)n0 * a.ldo + m;
-  const T *pi = reinterpret_cast<const T *>(a.up_in) + (size_t)n0 * a.ldo + m;
+  uint32_t gw[(NC + 1) / 2], pw[(NC + 1) / 2];
+  load_pairs<NC, T>(a, a.gate_in, m, n0, ok, gw);
+  load_pairs<NC, T>(a, a.up_in, m, n0, ok, pw);
 #pragma unroll
-  for (int j = 0; j < NC; ++j) {
-    const bool in = ok && n0 + j < a.n;
-    g[j] = in ? Elem<T>::to(gi[(size_t)j * a.ldo]) : 0.f;
-    p[j] = in ? Elem<T>::to(pi[(size_t)j * a.ldo]) : 0.f;
+  for (int j = 0; j < NC; j += 2) {
+    float x, y;
+    unpack2<T>(gw[j / 2], x, y);
+    g[j] = x;
+    if (j + 1 < NC) g[j + 1] = y;
+    unpack2<T>(pw[j / 2], x, y);
+    p[j] = x;
+    if (j + 1 < NC) p[j + 1] = y;
   }
 }
 template <int NC, typename T>
@@ -346,19 +431,26 @@ PI_DEV void load_a(const Args &a, int map, int blk, int row0, uint32_t dst, Load
 }
 
 // ================================================================ CTA-pair kernel
-constexpr int kPairThreads = 384;  // producer, MMA issuer, 2 idle warps, 8 epilogue warps
+constexpr int kPairThreads = 384;  // producer, MMA issuer, L2 prefetcher, idle warp, 8 epilogue warps
 constexpr int kPairEpi = 8;
+constexpr int kLead = 2;           // MB = 2: K blocks that one accumulator block runs ahead of the other
 
-template <int NT>
+// A pair's tile is MB blocks of 256 features (128 per CTA) x NT columns.
+// MB = 1: the two accumulator buffers alternate between tiles.  MB = 2: both
+// belong to one tile, which halves the B reads per product.
+template <int EPI, int MB, int NT>
 struct PairShape {
   static constexpr int NB = NT / 2;            // B rows that one CTA of the pair loads
-  static constexpr int ABYTES = 16384;         // 128 rows x 128 bytes
+  static constexpr int ABYTES = MB * 16384;    // MB x 128 rows x 128 bytes
   static constexpr int STAGE = ABYTES + NB * 128;
-  static constexpr int NS = NT == 256 ? 6 : 8;
-  static constexpr int XCH_OFF = NS * STAGE;   // E_GLU: gate/up exchange, 4 warp pairs x 4 KB
-  static constexpr int CTRL_OFF = XCH_OFF + 16384;
+  static constexpr int XCH = EPI == E_GLU ? 16384 : 0;  // gate/up exchange, 4 warp pairs x 4 KB
+  static constexpr int FIT = (227 * 1024 - 1536 - XCH) / STAGE;
+  static constexpr int NS = FIT > 8 ? 8 : FIT;
+  static constexpr int XCH_OFF = NS * STAGE;
+  static constexpr int CTRL_OFF = XCH_OFF + XCH;
   static constexpr int SMEM = CTRL_OFF + 512 + 1024;  // + alignment slack
-  static constexpr uint32_t TMEM_COLS = 2 * NT;
+  static constexpr uint32_t TMEM_COLS = 2 * NT <= 256 ? 256 : 512;
+  static_assert(NS >= 2 * kLead || MB == 1, "ring too shallow");
   static_assert(SMEM <= 227 * 1024, "shared memory");
 };
 
@@ -389,12 +481,12 @@ PI_DEV TileAt tile_at(const Args &a, int t) {
   return r;
 }
 
-template <int EPI, int AMN, int BMN, int NT, typename T>
+template <int EPI, int AMN, int BMN, int MB, int NT, typename T>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     pair_gemm_kernel(const __grid_constant__ Args a) {
-  using S = PairShape<NT>;
+  using S = PairShape<EPI, MB, NT>;
   constexpr bool I8 = EPI == E_I8;
-  constexpr int MROWS = EPI == E_GLU ? 64 : 128;  // features of one CTA's half tile
+  constexpr int MROWS = EPI == E_GLU ? 64 : 128;  // features of one CTA's half block
   extern __shared__ unsigned char smem_raw[];
   // the same offset in both CTAs of the pair (the dynamic shared window starts at the same place)
   unsigned char *smem = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -425,6 +517,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   tc_fence_after();
   const uint32_t tmem = C.tmem;
   volatile int *abort_flag = &C.abort_flag;
+  // accumulator block b of this CTA's tc-th tile: its buffer, and the parity of the buffer's tc-th use
+  auto buf_of = [](int tc, int b) { return MB == 1 ? tc & 1 : b; };
+  auto par_of = [](int tc) { return (unsigned)(MB == 1 ? (tc >> 1) & 1 : tc & 1); };
+  constexpr int FIRST_REUSE = MB == 1 ? 2 : 1;
 
   pdl_wait();
   pdl_launch_dependents();
@@ -432,15 +528,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   if (warp == 0) {
     // ------------------------------------------------------------ producer (one lane)
     if (lane == 0) {
-      long long it = 0;
+      int it = 0, s = 0;
+      unsigned ph = 0;
       bool ok = true;
       for (int t = pair; t < tiles && ok; t += npairs) {
         const TileAt at = tile_at(a, t);
-        const int row0 = (at.m * 2 + rank) * MROWS;
         const int col0 = at.n * NT + rank * S::NB;
-        for (int kb = 0; kb < a.kb; ++kb, ++it) {
-          const int s = (int)(it % S::NS);
-          const unsigned ph = (unsigned)((it / S::NS) & 1);
+        for (int kb = 0; kb < a.kb; ++kb) {
           if (it >= S::NS && !mbar_wait_cluster(&C.empty[s], ph ^ 1u, abort_flag, a.status)) {
             ok = false;
             break;
@@ -450,126 +544,193 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           if (rank == 0) mbar_expect_tx(&C.full[s], 2 * S::STAGE);
           int map, blk;
           k_at(a, at.prob, kb, map, blk);
-          load_a<EPI, AMN>(a, map, blk, row0, dst,
-                           [&](uint32_t d, const CUtensorMap *tm, int x, int y) { tma_load_2d_pair(d, tm, x, y, bar); });
+          auto load = [&](uint32_t d, const CUtensorMap *tm, int x, int y) { tma_load_2d_pair(d, tm, x, y, bar); };
+#pragma unroll
+          for (int b = 0; b < MB; ++b)
+            load_a<EPI, AMN>(a, map, blk, ((at.m * MB + b) * 2 + rank) * MROWS, dst + b * 16384, load);
           const CUtensorMap *tb = &a.mb[map];
           if constexpr (BMN) {
 #pragma unroll
-            for (int h = 0; h < S::NB / 64; ++h)
-              tma_load_2d_pair(dst + S::ABYTES + h * 8192, tb, col0 + h * 64, blk * 64, bar);
+            for (int h = 0; h < S::NB / 64; ++h) load(dst + S::ABYTES + h * 8192, tb, col0 + h * 64, blk * 64);
           } else {
-            tma_load_2d_pair(dst + S::ABYTES, tb, blk * (I8 ? 128 : 64), col0, bar);
+            load(dst + S::ABYTES, tb, blk * (I8 ? 128 : 64), col0);
           }
+          it = it < S::NS ? it + 1 : it;
+          if (++s == S::NS) s = 0, ph ^= 1u;
         }
       }
       // the MMAs that read the last stages have finished before this CTA may go
-      for (long long j = it > S::NS ? it - S::NS : 0; j < it && ok; ++j)
-        ok = mbar_wait_cluster(&C.empty[j % S::NS], (unsigned)((j / S::NS) & 1), abort_flag, a.status);
+      for (int j = 0; j < it && ok; ++j) {
+        if (--s < 0) s = S::NS - 1, ph ^= 1u;
+        ok = mbar_wait_cluster(&C.empty[s], ph, abort_flag, a.status);
+      }
     }
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer (one lane of the leader CTA)
     if (rank == 0 && lane == 0) {
-      long long it = 0;
-      int tc = 0;
+      int tc = 0, s = 0;
+      unsigned ph = 0;
       bool ok = true;
-      for (int t = pair; t < tiles && ok; t += npairs, ++tc) {
-        const int b = tc & 1;
-        if (tc >= 2 && !mbar_wait_cluster(&C.accfree[b], (unsigned)(((tc >> 1) & 1) ^ 1), abort_flag, a.status)) break;
+      auto wait_full = [&](int st, unsigned p) { return mbar_wait_cluster(&C.full[st], p, abort_flag, a.status); };
+      auto wait_free = [&](int b) {
+        const bool r = tc < FIRST_REUSE ||
+                       mbar_wait_cluster(&C.accfree[buf_of(tc, b)], par_of(tc) ^ 1u, abort_flag, a.status);
         tc_fence_after();
-        const uint32_t acc = tmem + (uint32_t)(b * NT);
-        for (int kb = 0; kb < a.kb; ++kb, ++it) {
-          const int s = (int)(it % S::NS);
-          if (!mbar_wait_cluster(&C.full[s], (unsigned)((it / S::NS) & 1), abort_flag, a.status)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t st = su32(smem + s * S::STAGE);
+        return r;
+      };
+      auto issue = [&](int b, int st, bool first) {
+        const uint32_t base = su32(smem + st * S::STAGE);
+        const uint32_t acc = tmem + (uint32_t)(buf_of(tc, b) * NT);
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            mma<2, I8>(acc, operand_desc<AMN>(st, j), operand_desc<BMN>(st + S::ABYTES, j), a.idesc,
-                       (kb | j) ? 1u : 0u);
-          mma_commit_pair(&C.empty[s]);
+        for (int j = 0; j < 4; ++j)
+          mma<2, I8>(acc, operand_desc<AMN>(base + b * 16384, j), operand_desc<BMN>(base + S::ABYTES, j), a.idesc,
+                     (first && j == 0) ? 0u : 1u);
+      };
+      for (int t = pair; t < tiles && ok; t += npairs, ++tc) {
+        if (MB == 1) {
+          if (!(ok = wait_free(0))) break;
+          for (int kb = 0; kb < a.kb; ++kb) {
+            if (!(ok = wait_full(s, ph))) break;
+            tc_fence_after();
+            issue(0, s, kb == 0);
+            mma_commit_pair(&C.empty[s]);
+            if (++s == S::NS) s = 0, ph ^= 1u;
+          }
+          if (ok) mma_commit_pair(&C.accfull[buf_of(tc, 0)]);
+        } else {
+          // Block 0 runs kLead K blocks ahead of block 1 at both ends of the
+          // tile: its epilogue starts while block 1's last MMAs run, and
+          // block 1's epilogue ends under block 0's first MMAs of the next
+          // tile.
+          const int head = min(kLead, a.kb), tail = min(kLead, a.kb - head);
+          int kb = 0;
+          auto both = [&](int n, bool first, bool last) {  // n K blocks: all of block 0, then all of block 1
+            int s0 = s;
+            unsigned p0 = ph;
+            for (int i = 0; i < n && ok; ++i) {
+              if (!(ok = wait_full(s0, p0))) return;
+              tc_fence_after();
+              issue(0, s0, first && i == 0);
+              if (++s0 == S::NS) s0 = 0, p0 ^= 1u;
+            }
+            if (last) mma_commit_pair(&C.accfull[0]);
+            if (first && !(ok = wait_free(1))) return;
+            for (int i = 0; i < n; ++i) {
+              issue(1, s, first && i == 0);
+              mma_commit_pair(&C.empty[s]);
+              if (++s == S::NS) s = 0, ph ^= 1u;
+            }
+            kb += n;
+          };
+          if (!(ok = wait_free(0))) break;
+          both(head, true, tail == 0);
+          while (ok && kb < a.kb - tail) both(1, false, false);
+          if (ok && tail) both(tail, false, true);
+          if (ok) mma_commit_pair(&C.accfull[1]);
         }
-        if (ok) mma_commit_pair(&C.accfull[b]);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 2) {
+    // ------------------------------------------------------------ E_DGLU: brings the next tile's g and p into L2
+    if (EPI == E_DGLU && lane == 0) {
+      int tc = -1;
+      for (int t = pair; t < tiles; t += npairs, ++tc) {
+        if (tc >= 0 && !mbar_wait_cluster(&C.accfull[buf_of(tc, MB - 1)], par_of(tc), abort_flag, a.status)) break;
+        const TileAt at = tile_at(a, t);
+#pragma unroll
+        for (int b = 0; b < MB; ++b) {
+          const int row0 = ((at.m * MB + b) * 2 + rank) * MROWS;
+          if (row0 >= a.m) continue;
+          prefetch_l2_2d(&a.ma[1], row0, at.n * NT);
+          prefetch_l2_2d(&a.ma[2], row0, at.n * NT);
+        }
       }
     }
     __syncwarp();
   } else if (warp >= 4) {
     // ------------------------------------------------------------ epilogue: lane quarter q, column half h
     const int q = warp & 3, h = (warp - 4) >> 2;
-    const int lrow = q * 32 + lane;  // row of this CTA's half tile
+    const int lrow = q * 32 + lane;  // row of this CTA's half block
     int tc = 0;
-    for (int t = pair; t < tiles; t += npairs, ++tc) {
+    bool go = true;
+    for (int t = pair; t < tiles && go; t += npairs, ++tc) {
       const TileAt at = tile_at(a, t);
-      const int b = tc & 1;
-      bool ok = __all_sync(0xffffffffu, mbar_wait_cluster(&C.accfull[b], (unsigned)((tc >> 1) & 1), abort_flag, a.status));
-      if constexpr (EPI == E_GLU) {
-        // the exchange below needs all 8 warps: agree on going on
-        uint32_t bad;
-        asm volatile(
-            "{\n .reg .pred p, r;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred r, 1, 256, p;\n"
-            " selp.u32 %0, 1, 0, r;\n}\n"
-            : "=r"(bad)
-            : "r"(ok ? 0u : 1u)
-            : "memory");
-        ok = !bad;
-      }
-      if (!ok) break;
-      tc_fence_after();
-      const uint32_t tbase = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * NT + h * (NT / 2));
-      const int n0 = at.n * NT + h * (NT / 2);
-      if constexpr (EPI == E_GLU) {
-        // lanes 0..63 hold gate rows, lanes 64..127 the up rows of the same
-        // neurons: warps q and q + 2 swap half a chunk through shared memory
-        // and each finishes the other half
-        const int neuron = (at.m * 2 + rank) * 64 + (q & 1) * 32 + lane;
-        const bool in = neuron < a.m;
-        const bool is_up = q >= 2;
-        float *xb = reinterpret_cast<float *>(smem + S::XCH_OFF) + (h * 2 + (q & 1)) * 1024;
-        void *keep = is_up ? a.up_out : a.gate_out;
 #pragma unroll 1
-        for (int c = 0; c < NT / 32; ++c) {
-          float v[16];
-          tmem_ld16(tbase + c * 16, v);
-          float *buf = xb + (c & 1) * 512;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) buf[(is_up ? 256 : 0) + j * 32 + lane] = is_up ? v[j] : v[8 + j];
-          if (keep) put_t<16, T>(a, keep, neuron, n0 + c * 16, in, v);
-          asm volatile("bar.sync %0, 64;" ::"r"(2 + h * 2 + (q & 1)) : "memory");
-          float mine[8], other[8], o[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            mine[j] = is_up ? v[8 + j] : v[j];
-            other[j] = buf[(is_up ? 0 : 256) + j * 32 + lane];
-          }
-          if (is_up) glu<8>(a.act, other, mine, o);
-          else glu<8>(a.act, mine, other, o);
-          put_t<8, T>(a, a.out[0], neuron, n0 + c * 16 + (is_up ? 8 : 0), in, o);
+      for (int blk = 0; blk < MB; ++blk) {
+        const int b = buf_of(tc, blk);
+        bool ok = __all_sync(0xffffffffu, mbar_wait_cluster(&C.accfull[b], par_of(tc), abort_flag, a.status));
+        if constexpr (EPI == E_GLU) {
+          // the exchange below needs all 8 warps: agree on going on
+          uint32_t bad;
+          asm volatile(
+              "{\n .reg .pred p, r;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred r, 1, 256, p;\n"
+              " selp.u32 %0, 1, 0, r;\n}\n"
+              : "=r"(bad)
+              : "r"(ok ? 0u : 1u)
+              : "memory");
+          ok = !bad;
         }
-      } else {
-        const int m = (at.m * 2 + rank) * 128 + lrow;
-        const bool in = m < a.m;
+        if (!ok) {
+          go = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t tbase = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * NT + h * (NT / 2));
+        const int n0 = at.n * NT + h * (NT / 2);
+        const int half_row0 = ((at.m * MB + blk) * 2 + rank) * MROWS;
+        if constexpr (EPI == E_GLU) {
+          // lanes 0..63 hold gate rows, lanes 64..127 the up rows of the same
+          // neurons: warps q and q + 2 swap half a chunk through shared memory
+          // and each finishes the other half
+          const int neuron = half_row0 + (q & 1) * 32 + lane;
+          const bool in = neuron < a.m;
+          const bool is_up = q >= 2;
+          float *xb = reinterpret_cast<float *>(smem + S::XCH_OFF) + (h * 2 + (q & 1)) * 1024;
+          void *keep = is_up ? a.up_out : a.gate_out;
 #pragma unroll 1
-        for (int c = 0; c < NT / 32; ++c) {
-          float v[16];
-          const int nc = n0 + c * 16;
-          if constexpr (EPI == E_DGLU) {
-            float g[16], p[16];
-            load_gp<16, T>(a, m, nc, in, g, p);
+          for (int c = 0; c < NT / 32; ++c) {
+            float v[16];
             tmem_ld16(tbase + c * 16, v);
-            epi_dglu<16, T>(a, m, nc, in, v, g, p);
-          } else {
-            tmem_ld16(tbase + c * 16, v);
-            if constexpr (EPI == E_I8) epi_i8<16>(a, m, nc, in, v);
-            else put_cols<16>(a, a.out[at.prob], m, nc, in, v, a.out_type, a.accumulate);
+            float *buf = xb + (c & 1) * 512;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) buf[(is_up ? 256 : 0) + j * 32 + lane] = is_up ? v[j] : v[8 + j];
+            if (keep) put_t<16, T>(a, keep, neuron, n0 + c * 16, in, v);
+            asm volatile("bar.sync %0, 64;" ::"r"(2 + h * 2 + (q & 1)) : "memory");
+            float mine[8], other[8], o[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              mine[j] = is_up ? v[8 + j] : v[j];
+              other[j] = buf[(is_up ? 0 : 256) + j * 32 + lane];
+            }
+            if (is_up) glu<8>(a.act, other, mine, o);
+            else glu<8>(a.act, mine, other, o);
+            put_t<8, T>(a, a.out[0], neuron, n0 + c * 16 + (is_up ? 8 : 0), in, o);
+          }
+        } else {
+          const int m = half_row0 + lrow;
+          const bool in = m < a.m;
+#pragma unroll 1
+          for (int c = 0; c < NT / 32; ++c) {
+            float v[16];
+            const int nc = n0 + c * 16;
+            if constexpr (EPI == E_DGLU) {
+              float g[16], p[16];
+              load_gp<16, T>(a, m, nc, in, g, p);
+              tmem_ld16(tbase + c * 16, v);
+              epi_dglu<16, T>(a, m, nc, in, v, g, p);
+            } else {
+              tmem_ld16(tbase + c * 16, v);
+              if constexpr (EPI == E_I8) epi_i8<16>(a, m, nc, in, v);
+              else put_cols<16, T>(a, a.out[at.prob], m, nc, in, v, a.out_type, a.accumulate);
+            }
           }
         }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(mapa(su32(&C.accfree[b]), 0));
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(mapa(su32(&C.accfree[b]), 0));
     }
   }
   if (*abort_flag) __nanosleep(1000000);  // copies in flight land before the CTA goes
@@ -738,7 +899,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2) split_gemm_kernel(const __gr
           load_gp<1, T>(a, m, col0 + n, in, g, p);
           epi_dglu<1, T>(a, m, col0 + n, in, v, g, p);
         } else {
-          put_cols<1>(a, a.out[0], m, col0 + n, in, v, a.out_type, a.accumulate);
+          put_cols<1, T>(a, a.out[0], m, col0 + n, in, v, a.out_type, a.accumulate);
         }
       }
     }
