@@ -1,18 +1,15 @@
-// pi_dense.cu -- C ABI of the dense block operators: the gated feed-forward
-// block and its gradients, the norms around a block, the 8-bit product.  Host
-// validation, workspace layout and kernel dispatch; the declarations and
+// pi_dense.cu -- C ABI of the dense products: the gated feed-forward block and
+// its gradients, the 8-bit product.  Host validation, workspace layout and kernel dispatch; the declarations and
 // argument contracts live in include/pi_ffn.h.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
-#include <cmath>
 #include <cstdint>
 #include <new>
 
 #include "pi_ffn.h"
 #include "pi_gemm.cuh"
 #include "pi_host.cuh"
-#include "pi_norm.cuh"
 
 struct pi_gated_ffn {
   pi_gated_ffn_desc d;
@@ -27,52 +24,9 @@ namespace {
 
 using namespace pi::host;
 namespace GM = pi::gemm;
-namespace NM = pi::norm;
 
-constexpr size_t kHeader = 256;        // status word
-constexpr int kMaxNormD = 16384;
 constexpr int kMaxI8K = 131056;        // 128 * 128 * K stays below 2^31
-constexpr int kMaxTokens = 1 << 24;    // tile and row indices stay in 32 bits
 constexpr int kMaxDim = 1 << 20;
-
-int cdiv(int a, int b) { return (a + b - 1) / b; }
-bool overlap(const void *p, size_t pn, const void *q, size_t qn) {
-  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
-  return p && q && a < b + qn && b < a + pn;
-}
-bool is_half(int t) { return t == PI_DT_F16 || t == PI_DT_BF16; }
-bool is_type(int t) { return t == PI_DT_F32 || is_half(t); }
-size_t type_size(int t) { return t == PI_DT_F32 ? 4 : 2; }
-
-#define PI_TRY(call)                                   \
-  do {                                                 \
-    if ((call) != cudaSuccess) return PI_ERR_CUDA;     \
-  } while (0)
-
-// ---------------------------------------------------------------- launching
-template <typename KArg>
-cudaError_t launch1(void (*kern)(KArg), dim3 grid, int threads, size_t smem, int cluster, DeviceOnce *once,
-                    cudaStream_t st, const KArg &arg) {
-  if (once) {
-    const cudaError_t e = once->ensure(
-        [&] { return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem); });
-    if (e != cudaSuccess) return e;
-  }
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute at[2];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  at[1].id = cudaLaunchAttributeClusterDimension;
-  at[1].val.clusterDim.x = (unsigned)cluster;
-  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = cluster > 0 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kern, arg);
-}
 
 template <int EPI, int AMN, int BMN, int MB, int NT, typename T>
 cudaError_t pair_launch(const GM::Args &a, int sms, cudaStream_t st) {
@@ -80,13 +34,13 @@ cudaError_t pair_launch(const GM::Args &a, int sms, cudaStream_t st) {
   const long long tiles = (long long)a.nprob * a.mt * a.nt;
   const int pairs = (int)(tiles < sms / 2 ? tiles : sms / 2);
   return launch1(GM::pair_gemm_kernel<EPI, AMN, BMN, MB, NT, T>, dim3(2 * pairs), GM::kPairThreads,
-                 GM::PairShape<EPI, MB, NT>::SMEM, 0, &once, st, a);
+                 GM::PairShape<EPI, MB, NT>::SMEM, 0, &once, st, a, GM::PairShape<EPI, MB, NT>::SMEM);
 }
 template <int EPI, int AMN, int NT, typename T>
 cudaError_t split_launch(const GM::Args &a, int split, cudaStream_t st) {
   static DeviceOnce once;
   return launch1(GM::split_gemm_kernel<EPI, AMN, NT, T>, dim3((unsigned)(a.mt * a.nt * split)), GM::kSplitThreads,
-                 GM::SplitShape<NT>::SMEM, split, &once, st, a);
+                 GM::SplitShape<NT>::SMEM, split, &once, st, a, GM::SplitShape<NT>::SMEM);
 }
 
 // How a product runs.  nt: token columns of a tile; mb: 256-feature blocks of
@@ -213,7 +167,7 @@ pi_status ffn_forward(const pi_gated_ffn *h, const void *u, int tokens, void *y,
     a.act = h->d.act;
     a.gate_out = gate, a.up_out = up;
     a.status = w.status;
-    PI_TRY((run_plan<GM::E_GLU, 0, T>(a, p, dt, 64, sms, st)));
+    PI_CUDA((run_plan<GM::E_GLU, 0, T>(a, p, dt, 64, sms, st)));
   }
   GM::Args a{};
   a.m = d, a.n = tokens, a.nprob = 1;
@@ -226,7 +180,7 @@ pi_status ffn_forward(const pi_gated_ffn *h, const void *u, int tokens, void *y,
   a.out_type = dt;
   a.early_a = 1;  // the product above does not write the weights
   a.status = w.status;
-  PI_TRY((run_plan<GM::E_STORE, 1, T>(a, p, dt, 128, sms, st)));
+  PI_CUDA((run_plan<GM::E_STORE, 1, T>(a, p, dt, 128, sms, st)));
   return PI_OK;
 }
 
@@ -254,7 +208,7 @@ pi_status ffn_backward(const pi_gated_ffn *h, const void *u, const void *gate, c
     a.gate_in = gate, a.up_in = up;
     a.gate_out = w.dg, a.up_out = w.dp;
     a.status = w.status;
-    PI_TRY((run_plan<GM::E_DGLU, 0, T>(a, p, dt, 128, sms, st)));
+    PI_CUDA((run_plan<GM::E_DGLU, 0, T>(a, p, dt, 128, sms, st)));
   }
   {
     // the matrices' gradients, [f x d] each: lanes along d, columns along f, K = tokens
@@ -286,7 +240,7 @@ pi_status ffn_backward(const pi_gated_ffn *h, const void *u, const void *gate, c
       a.mt = cdiv(d, 256 * mb);
       a.nt = cdiv(f, 256);
       a.idesc = idesc(dt, false, 256, 256, 1, 1);
-      PI_TRY((mb == 2 ? pair_launch<GM::E_STORE, 1, 1, 2, 256, T>(a, sms, st)
+      PI_CUDA((mb == 2 ? pair_launch<GM::E_STORE, 1, 1, 2, 256, T>(a, sms, st)
                       : pair_launch<GM::E_STORE, 1, 1, 1, 256, T>(a, sms, st)));
     }
   }
@@ -305,44 +259,10 @@ pi_status ffn_backward(const pi_gated_ffn *h, const void *u, const void *gate, c
     a.out_type = dt;
     a.early_a = 1;  // the products above do not write the weights
     a.status = w.status;
-    PI_TRY((run_plan<GM::E_STORE, 1, T>(a, p, dt, 128, sms, st)));
+    PI_CUDA((run_plan<GM::E_STORE, 1, T>(a, p, dt, 128, sms, st)));
   }
   return PI_OK;
 }
-
-// ---------------------------------------------------------------- norms
-// Threads and chunks per thread of a row of d elements: up to 512 threads
-// with 4-element chunks, more chunks for longer rows.
-struct RowShape {
-  int threads, ch;
-};
-RowShape row_shape(int d) {
-  const int chunks = d / 4;
-  int ch = 1;
-  while (ch < 8 && cdiv(chunks, ch) > 512) ch *= 2;
-  return RowShape{cdiv(cdiv(chunks, ch), 32) * 32, ch};
-}
-pi_status check_norm(const pi_block_norm_desc *D) {
-  if (!D || D->d_model <= 0 || !is_type(D->y_dtype) || !is_type(D->u_dtype)) return PI_ERR_INVALID_ARG;
-  if (!(D->eps > 0.f) || !std::isfinite(D->eps) || !std::isfinite(D->residual_scale) || !std::isfinite(D->branch_scale))
-    return PI_ERR_INVALID_ARG;
-  if (D->w_post && !D->post_norm) return PI_ERR_INVALID_ARG;
-  if (D->gate && D->tokens_per_gate <= 0) return PI_ERR_INVALID_ARG;
-  if (D->d_model % 8 || D->d_model > kMaxNormD) return PI_ERR_UNSUPPORTED;
-  if ((D->w_post && !aligned16(D->w_post)) || (D->w_pre && !aligned16(D->w_pre)) || (D->gate && !aligned16(D->gate)))
-    return PI_ERR_MISALIGNED;
-  return PI_OK;
-}
-// Blocks of the backward kernel: enough to fill the machine, each with a run of rows.
-int norm_bwd_blocks(int d, int tokens, int sms) {
-  const RowShape r = row_shape(d);
-  int per_sm = 1024 / r.threads;
-  if (per_sm < 1) per_sm = 1;
-  if (per_sm > 8) per_sm = 8;
-  const int g = sms * per_sm;
-  return tokens < g ? tokens : g;
-}
-size_t norm_ws_bytes(int d, int G) { return kHeader + (size_t)G * d * 4 * 4; }
 
 }  // namespace
 
@@ -412,7 +332,7 @@ pi_status pi_gated_ffn_backward(pi_gated_ffn_t h, const void *u, const void *gat
     void *const dw[] = {dw_gate, dw_up, dw_down_t};
     if (!acc)
       for (void *p : dw)
-        if (p) PI_TRY(cudaMemsetAsync(p, 0, n, st));
+        if (p) PI_CUDA(cudaMemsetAsync(p, 0, n, st));
     return PI_OK;
   }
   FfnWs w;
@@ -425,162 +345,7 @@ pi_status pi_gated_ffn_backward(pi_gated_ffn_t h, const void *u, const void *gat
                                            w, st);
 }
 
-// ====================================================================== norms around a block
-pi_status pi_block_norm_forward(const pi_block_norm_desc *desc, const float *x, const void *y, int tokens,
-                                float *x_out, void *u, float *rstd_post, float *rstd_pre, pi_stream_t stream) {
-  const pi_status s = check_norm(desc);
-  if (s != PI_OK) return s;
-  if (tokens < 0 || tokens > kMaxTokens) return PI_ERR_UNSUPPORTED;
-  if (tokens == 0) return PI_OK;
-  if (!x || (!x_out && !u)) return PI_ERR_INVALID_ARG;
-  if ((rstd_post && !(y && desc->post_norm)) || (rstd_pre && !u)) return PI_ERR_INVALID_ARG;
-  const void *ptrs[] = {x, y, x_out, u, rstd_post, rstd_pre};
-  for (const void *p : ptrs)
-    if (p && !aligned16(p)) return PI_ERR_MISALIGNED;
-  const size_t n = (size_t)tokens * desc->d_model;
-  if (x_out != x && overlap(x_out, n * 4, x, n * 4)) return PI_ERR_INVALID_ARG;
-  if (overlap(x_out, n * 4, y, n * type_size(desc->y_dtype)) || overlap(u, n * type_size(desc->u_dtype), x, n * 4) ||
-      overlap(u, n * type_size(desc->u_dtype), x_out, n * 4) ||
-      overlap(u, n * type_size(desc->u_dtype), y, n * type_size(desc->y_dtype)))
-    return PI_ERR_INVALID_ARG;
-  NM::FwdArgs a{};
-  a.x = x, a.y = y;
-  a.w_post = desc->w_post, a.w_pre = desc->w_pre, a.gate = desc->gate;
-  a.x_out = x_out, a.u = u, a.rstd_post = rstd_post, a.rstd_pre = rstd_pre;
-  a.tokens = tokens, a.d = desc->d_model, a.tokens_per_gate = desc->tokens_per_gate;
-  a.y_type = desc->y_dtype, a.u_type = desc->u_dtype, a.post_norm = desc->post_norm ? 1 : 0;
-  a.eps = desc->eps, a.alpha = desc->residual_scale, a.beta = desc->branch_scale;
-  const int sms = device_sm_count();
-  if (sms <= 0) return PI_ERR_CUDA;
-  const RowShape r = row_shape(a.d);
-  const int per_sm = 2048 / r.threads > 32 ? 32 : 2048 / r.threads;
-  const dim3 g(tokens < sms * per_sm ? tokens : sms * per_sm);
-  cudaStream_t st = (cudaStream_t)stream;
-  switch (r.ch) {
-  case 1:
-    PI_TRY(launch1(NM::norm_fwd_kernel<1>, g, r.threads, 0, 0, nullptr, st, a));
-    break;
-  case 2:
-    PI_TRY(launch1(NM::norm_fwd_kernel<2>, g, r.threads, 0, 0, nullptr, st, a));
-    break;
-  case 4:
-    PI_TRY(launch1(NM::norm_fwd_kernel<4>, g, r.threads, 0, 0, nullptr, st, a));
-    break;
-  default:
-    PI_TRY(launch1(NM::norm_fwd_kernel<8>, g, r.threads, 0, 0, nullptr, st, a));
-  }
-  return PI_OK;
-}
-
-pi_status pi_block_norm_workspace_size(const pi_block_norm_desc *desc, int max_tokens, size_t *bytes) {
-  const pi_status s = check_norm(desc);
-  if (s != PI_OK) return s;
-  if (!bytes) return PI_ERR_INVALID_ARG;
-  if (max_tokens < 0 || max_tokens > kMaxTokens) return PI_ERR_UNSUPPORTED;
-  const int sms = device_sm_count();
-  if (sms <= 0) return PI_ERR_CUDA;
-  *bytes = norm_ws_bytes(desc->d_model, norm_bwd_blocks(desc->d_model, max_tokens, sms));
-  return PI_OK;
-}
-
-pi_status pi_block_norm_backward(const pi_block_norm_desc *desc, const float *x_out, const void *y,
-                                 const float *rstd_post, const float *rstd_pre, const void *du, const float *dx_out,
-                                 int tokens, float *dx, void *dy, float *dw_post, float *dw_pre, float *dgate,
-                                 unsigned flags, void *ws, size_t ws_bytes, pi_stream_t stream) {
-  pi_status s = check_norm(desc);
-  if (s != PI_OK) return s;
-  if (flags & ~(unsigned)PI_GRAD_ACCUMULATE) return PI_ERR_INVALID_ARG;
-  if ((dw_post && !desc->post_norm) || (dgate && !desc->gate)) return PI_ERR_INVALID_ARG;
-  if (tokens < 0 || tokens > kMaxTokens) return PI_ERR_UNSUPPORTED;
-  if (tokens) {
-    if (!du && !dx_out) return PI_ERR_INVALID_ARG;
-    if (du ? (!x_out || !rstd_pre) : dw_pre != nullptr) return PI_ERR_INVALID_ARG;
-    if (y ? (desc->post_norm && !rstd_post) : (dy || dw_post || dgate)) return PI_ERR_INVALID_ARG;
-  }
-  const void *ptrs[] = {x_out, y, rstd_post, rstd_pre, du, dx_out, dx, dy, dw_post, dw_pre, dgate};
-  for (const void *p : ptrs)
-    if (p && !aligned16(p)) return PI_ERR_MISALIGNED;
-  const int d = desc->d_model;
-  const size_t n = (size_t)tokens * d, nx = n * 4, ny = n * type_size(desc->y_dtype), nu = n * type_size(desc->u_dtype);
-  if ((dx != dx_out && overlap(dx, nx, dx_out, nx)) || overlap(dx, nx, x_out, nx) || overlap(dx, nx, y, ny) ||
-      overlap(dx, nx, du, nu) || overlap(dy, ny, x_out, nx) || (dy != y && overlap(dy, ny, y, ny)) ||
-      overlap(dy, ny, du, nu) || overlap(dy, ny, dx_out, nx) || overlap(dx, nx, dy, ny))
-    return PI_ERR_INVALID_ARG;
-  cudaStream_t st = (cudaStream_t)stream;
-  const int acc = (flags & PI_GRAD_ACCUMULATE) ? 1 : 0;
-  if (tokens == 0) {  // no tokens: the sums over them are zero (and there is no gate row)
-    if (!acc && dw_post) PI_TRY(cudaMemsetAsync(dw_post, 0, (size_t)d * 4, st));
-    if (!acc && dw_pre) PI_TRY(cudaMemsetAsync(dw_pre, 0, (size_t)d * 4, st));
-    return PI_OK;
-  }
-  if (!ws) return PI_ERR_WORKSPACE;
-  if (!aligned16(ws)) return PI_ERR_MISALIGNED;
-  const int sms = device_sm_count();
-  if (sms <= 0) return PI_ERR_CUDA;
-  const int G = norm_bwd_blocks(d, tokens, sms);
-  if (ws_bytes < norm_ws_bytes(d, G)) return PI_ERR_WORKSPACE;
-  float *part = reinterpret_cast<float *>(static_cast<char *>(ws) + kHeader);
-  NM::BwdArgs a{};
-  a.x_out = x_out, a.y = y, a.du = du, a.rstd_post = rstd_post, a.rstd_pre = rstd_pre, a.dx_out = dx_out;
-  a.w_post = desc->w_post, a.w_pre = desc->w_pre, a.gate = desc->gate;
-  a.dx = dx, a.dy = dy, a.dgate = dgate;
-  a.part_post = dw_post ? part : nullptr;
-  a.part_pre = dw_pre ? part + (size_t)G * d : nullptr;
-  a.part_gate = part + (size_t)2 * G * d;
-  a.tokens = tokens, a.d = d, a.tokens_per_gate = desc->tokens_per_gate;
-  a.y_type = desc->y_dtype, a.u_type = desc->u_dtype, a.post_norm = desc->post_norm ? 1 : 0;
-  a.accumulate = acc;
-  a.alpha = desc->residual_scale, a.beta = desc->branch_scale;
-  const RowShape r = row_shape(d);
-  switch (r.ch) {
-  case 1:
-    PI_TRY(launch1(NM::norm_bwd_kernel<1>, dim3(G), r.threads, 0, 0, nullptr, st, a));
-    break;
-  case 2:
-    PI_TRY(launch1(NM::norm_bwd_kernel<2>, dim3(G), r.threads, 0, 0, nullptr, st, a));
-    break;
-  case 4:
-    PI_TRY(launch1(NM::norm_bwd_kernel<4>, dim3(G), r.threads, 0, 0, nullptr, st, a));
-    break;
-  default:
-    PI_TRY(launch1(NM::norm_bwd_kernel<8>, dim3(G), r.threads, 0, 0, nullptr, st, a));
-  }
-  if (dw_post || dw_pre || dgate) {
-    NM::JoinArgs j{};
-    j.part_post = a.part_post, j.part_pre = a.part_pre, j.part_gate = a.part_gate;
-    j.dw_post = dw_post, j.dw_pre = dw_pre, j.dgate = dgate;
-    j.G = G, j.tokens = tokens, j.d = d, j.tokens_per_gate = desc->tokens_per_gate, j.accumulate = acc;
-    const dim3 g(cdiv(d, 32), dgate ? 2 + G - 1 : 2);
-    PI_TRY(launch1(NM::norm_join_kernel, g, 256, 0, 0, nullptr, st, j));
-  }
-  return PI_OK;
-}
-
 // ====================================================================== 8-bit product
-pi_status pi_quantize_i8(const void *x, int x_dtype, int rows, int k, int8_t *q, float *scales, pi_stream_t stream) {
-  if (k <= 0 || !is_type(x_dtype)) return PI_ERR_INVALID_ARG;
-  if (k % 16 || rows < 0 || rows > kMaxTokens || k > kMaxI8K) return PI_ERR_UNSUPPORTED;
-  if (rows == 0) return PI_OK;
-  if (!x || !q || !scales) return PI_ERR_INVALID_ARG;
-  if (!aligned16(x) || !aligned16(q) || !aligned16(scales)) return PI_ERR_MISALIGNED;
-  const int sms = device_sm_count();
-  if (sms <= 0) return PI_ERR_CUDA;
-  int threads = cdiv(cdiv(k, 8), 32) * 32;
-  if (threads > 1024) threads = 1024;
-  const int per_sm = 2048 / threads > 32 ? 32 : 2048 / threads;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(rows < sms * per_sm ? rows : sms * per_sm);
-  cfg.blockDim = dim3(threads);
-  cfg.stream = (cudaStream_t)stream;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  PI_TRY(cudaLaunchKernelEx(&cfg, NM::quantize_i8_kernel, x, x_dtype, rows, k, q, scales));
-  return PI_OK;
-}
-
 pi_status pi_matmul_i8_workspace_size(int tokens, int n, int k, size_t *bytes) {
   if (!bytes || n <= 0 || k <= 0) return PI_ERR_INVALID_ARG;
   if (k % 16 || k > kMaxI8K || n > kMaxDim || tokens < 0 || tokens > kMaxTokens) return PI_ERR_UNSUPPORTED;
@@ -615,7 +380,7 @@ pi_status pi_matmul_i8(const int8_t *xq, const float *x_scales, const int8_t *wq
   a.out_type = y_dtype;
   a.s_n = x_scales, a.s_m = w_scales, a.bias = bias;
   a.status = static_cast<int *>(ws);
-  PI_TRY((run_plan<GM::E_I8, 0, __half>(a, p, 0, 128, sms, (cudaStream_t)stream)));
+  PI_CUDA((run_plan<GM::E_I8, 0, __half>(a, p, 0, 128, sms, (cudaStream_t)stream)));
   return PI_OK;
 }
 

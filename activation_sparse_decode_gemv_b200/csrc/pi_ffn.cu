@@ -267,7 +267,6 @@ cudaError_t launch(void (*kern)(KArgs...), dim3 grid, dim3 block, cudaStream_t s
 }
 
 inline int nb_for(int B) { return B <= 1 ? 1 : B <= 2 ? 2 : B <= 4 ? 4 : 8; }
-inline int cdiv(int a, int b) { return (a + b - 1) / b; }
 
 template <int NB>
 cudaError_t pred_h_nb(int pt, dim3 g, cudaStream_t st, const void *p1, const void *u, int d, int r, int B, float *h) {
@@ -344,11 +343,6 @@ bool want_dense(const pi_ffn *h, int B, unsigned flags) {
   if (!(p > 0.0)) return false;
   return 1.0 - std::pow(1.0 - (p < 1.0 ? p : 1.0), (double)B) >= 0.75;
 }
-
-#define PI_CUDA(call)                      \
-  do {                                     \
-    if ((call) != cudaSuccess) return PI_ERR_CUDA; \
-  } while (0)
 
 // Test support (pi_debug_wait_fault): an entry of h that is never published,
 // and a shorter limit for every bounded wait of the fused and batch

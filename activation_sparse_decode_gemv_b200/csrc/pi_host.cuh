@@ -8,6 +8,13 @@
 #include <cstddef>
 #include <cstdint>
 
+#include "pi_ffn.h"
+
+#define PI_CUDA(call)                                   \
+  do {                                                 \
+    if ((call) != cudaSuccess) return PI_ERR_CUDA;     \
+  } while (0)
+
 namespace pi {
 namespace host {
 
@@ -77,6 +84,47 @@ inline bool map_2d(CUtensorMap *m, const void *base, bool fp16, uint64_t inner, 
              dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
              swz ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// ---------------------------------------------------------------- dense block operators
+constexpr size_t kHeader = 256;      // start of a workspace: its status word
+constexpr int kMaxTokens = 1 << 24;  // tile and row indices stay in 32 bits
+
+inline int cdiv(int a, int b) { return (a + b - 1) / b; }
+inline bool overlap(const void *p, size_t pn, const void *q, size_t qn) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return p && q && a < b + qn && b < a + pn;
+}
+inline bool is_half(int t) { return t == PI_DT_F16 || t == PI_DT_BF16; }
+inline bool is_type(int t) { return t == PI_DT_F32 || is_half(t); }
+inline size_t type_size(int t) { return t == PI_DT_F32 ? 4 : 2; }
+
+// Launches a kernel with one argument as a programmatic dependent of the
+// work before it (the kernel waits by griddepcontrol.wait).  cluster: cluster
+// size, 0 for the kernel's own; once: set where the kernel uses dynamic shared
+// memory, up to max_smem.
+template <typename KArg>
+cudaError_t launch1(void (*kern)(KArg), dim3 grid, int threads, size_t smem, int cluster, DeviceOnce *once,
+                    cudaStream_t st, const KArg &arg, int max_smem = 224 * 1024) {
+  if (once) {
+    const cudaError_t e = once->ensure(
+        [&] { return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, max_smem); });
+    if (e != cudaSuccess) return e;
+  }
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = (unsigned)cluster;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = cluster > 0 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, arg);
 }
 
 }  // namespace host

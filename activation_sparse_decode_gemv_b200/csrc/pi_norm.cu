@@ -1,0 +1,267 @@
+// pi_norm.cu -- C ABI of the row-wise operators around a block: the norms with
+// gate, residual scale and residual add, their gradients, the 8-bit
+// quantiser.  Host validation, workspace layout and kernel dispatch.
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "pi_ffn.h"
+#include "pi_host.cuh"
+#include "pi_norm.cuh"
+
+namespace {
+
+using namespace pi::host;
+namespace NM = pi::norm;
+
+constexpr int kMaxNormD = 16384;
+constexpr int kMaxI8K = 131056;
+
+// ---------------------------------------------------------------- norms
+// Launch shape of the row kernels: up to 512 threads with ch chunks of 4
+// elements each, a ring of `rows` rows in shared memory (one row, refilled
+// once it is in registers, where two do not fit), `per_sm` blocks per SM.
+struct RowShape {
+  int threads, ch, rows, per_sm;
+  size_t smem;
+};
+constexpr size_t kRowSmem = 200 * 1024;  // of the 227 KB per block; the rest is L1 for the column factors
+RowShape row_shape(int d, int bytes_per_element, bool backward) {
+  const int chunks = d / 4;
+  RowShape r{};
+  r.ch = cdiv(chunks, 512);
+  if (r.ch > 4) r.ch = 8;
+  r.threads = cdiv(cdiv(chunks, r.ch), 32) * 32;
+  const size_t row = (size_t)r.threads * r.ch * 4 * bytes_per_element;
+  r.rows = 2 * row <= kRowSmem ? 2 : 1;
+  r.smem = r.rows * row;
+  r.per_sm = (int)(kRowSmem / (r.smem + 1024));
+  // threads that the registers hold: forward up to 38, 64, 64, 115, 128 a thread
+  // for ch = 1, 2, 3, 4, 8; backward 98, 102, 126, 128
+  const int fits = r.ch > 3 ? 512 : backward ? (r.ch == 1 ? 640 : r.ch == 2 ? 608 : 512) : r.ch == 1 ? 1536 : 1024;
+  const int by_threads = fits / r.threads;
+  if (r.per_sm > by_threads) r.per_sm = by_threads;
+  if (r.per_sm < 1) r.per_sm = 1;
+  if (r.per_sm > 16) r.per_sm = 16;
+  return r;
+}
+pi_status check_norm(const pi_block_norm_desc *D) {
+  if (!D || D->d_model <= 0 || !is_type(D->y_dtype) || !is_type(D->u_dtype)) return PI_ERR_INVALID_ARG;
+  if (!(D->eps > 0.f) || !std::isfinite(D->eps) || !std::isfinite(D->residual_scale) || !std::isfinite(D->branch_scale))
+    return PI_ERR_INVALID_ARG;
+  if (D->w_post && !D->post_norm) return PI_ERR_INVALID_ARG;
+  if (D->gate && D->tokens_per_gate <= 0) return PI_ERR_INVALID_ARG;
+  if (D->d_model % 8 || D->d_model > kMaxNormD) return PI_ERR_UNSUPPORTED;
+  if ((D->w_post && !aligned16(D->w_post)) || (D->w_pre && !aligned16(D->w_pre)) || (D->gate && !aligned16(D->gate)))
+    return PI_ERR_MISALIGNED;
+  return PI_OK;
+}
+// Blocks of the backward kernel: enough to fill the machine, but four rows
+// each where the tokens allow, since a block leaves a row of partials behind.
+// At most kBwdBlocks per SM whatever the types, so that a workspace sized for
+// more tokens serves fewer.
+constexpr int kBwdBlocks = 8;
+int norm_bwd_blocks(int per_sm, int tokens, int sms) {
+  if (per_sm > kBwdBlocks) per_sm = kBwdBlocks;
+  int g = cdiv(tokens, 4);
+  if (g < sms) g = sms;
+  if (g > sms * per_sm) g = sms * per_sm;
+  if (g > NM::kMaxBwdBlocks) g = NM::kMaxBwdBlocks;
+  return tokens < g ? tokens : g;
+}
+// types: 3 * y + u
+template <int CH, int R>
+pi_status fwd_launch(const NM::FwdArgs &a, dim3 g, const RowShape &r, cudaStream_t st) {
+  static void (*const kern[9])(NM::FwdArgs) = {
+      NM::norm_fwd_kernel<CH, R, 0, 0>, NM::norm_fwd_kernel<CH, R, 0, 1>, NM::norm_fwd_kernel<CH, R, 0, 2>,
+      NM::norm_fwd_kernel<CH, R, 1, 0>, NM::norm_fwd_kernel<CH, R, 1, 1>, NM::norm_fwd_kernel<CH, R, 1, 2>,
+      NM::norm_fwd_kernel<CH, R, 2, 0>, NM::norm_fwd_kernel<CH, R, 2, 1>, NM::norm_fwd_kernel<CH, R, 2, 2>};
+  static DeviceOnce once[9];
+  const int k = 3 * a.y_type + a.u_type;
+  PI_CUDA(launch1(kern[k], g, r.threads, r.smem, 0, &once[k], st, a));
+  return PI_OK;
+}
+template <int CH, int R>
+pi_status bwd_launch(const NM::BwdArgs &a, int G, const RowShape &r, cudaStream_t st) {
+  static void (*const kern[9])(NM::BwdArgs) = {
+      NM::norm_bwd_kernel<CH, R, 0, 0>, NM::norm_bwd_kernel<CH, R, 0, 1>, NM::norm_bwd_kernel<CH, R, 0, 2>,
+      NM::norm_bwd_kernel<CH, R, 1, 0>, NM::norm_bwd_kernel<CH, R, 1, 1>, NM::norm_bwd_kernel<CH, R, 1, 2>,
+      NM::norm_bwd_kernel<CH, R, 2, 0>, NM::norm_bwd_kernel<CH, R, 2, 1>, NM::norm_bwd_kernel<CH, R, 2, 2>};
+  static DeviceOnce once[9];
+  const int k = 3 * a.y_type + a.u_type;
+  PI_CUDA(launch1(kern[k], dim3(G), r.threads, r.smem, 0, &once[k], st, a));
+  return PI_OK;
+}
+size_t norm_ws_bytes(int d, int G) { return kHeader + (size_t)G * d * 4 * 4; }  // dw_post, dw_pre, 2 gate rows
+
+}  // namespace
+
+extern "C" {
+
+// ====================================================================== norms around a block
+pi_status pi_block_norm_forward(const pi_block_norm_desc *desc, const float *x, const void *y, int tokens,
+                                float *x_out, void *u, float *rstd_post, float *rstd_pre, pi_stream_t stream) {
+  const pi_status s = check_norm(desc);
+  if (s != PI_OK) return s;
+  if (tokens < 0 || tokens > kMaxTokens) return PI_ERR_UNSUPPORTED;
+  if (tokens == 0) return PI_OK;
+  if (!x || (!x_out && !u)) return PI_ERR_INVALID_ARG;
+  if ((rstd_post && !(y && desc->post_norm)) || (rstd_pre && !u)) return PI_ERR_INVALID_ARG;
+  const void *ptrs[] = {x, y, x_out, u, rstd_post, rstd_pre};
+  for (const void *p : ptrs)
+    if (p && !aligned16(p)) return PI_ERR_MISALIGNED;
+  const size_t n = (size_t)tokens * desc->d_model;
+  if (x_out != x && overlap(x_out, n * 4, x, n * 4)) return PI_ERR_INVALID_ARG;
+  if (overlap(x_out, n * 4, y, n * type_size(desc->y_dtype)) || overlap(u, n * type_size(desc->u_dtype), x, n * 4) ||
+      overlap(u, n * type_size(desc->u_dtype), x_out, n * 4) ||
+      overlap(u, n * type_size(desc->u_dtype), y, n * type_size(desc->y_dtype)))
+    return PI_ERR_INVALID_ARG;
+  NM::FwdArgs a{};
+  a.x = x, a.y = y;
+  a.w_post = desc->w_post, a.w_pre = desc->w_pre, a.gate = desc->gate;
+  a.x_out = x_out, a.u = u, a.rstd_post = rstd_post, a.rstd_pre = rstd_pre;
+  a.tokens = tokens, a.d = desc->d_model, a.tokens_per_gate = desc->tokens_per_gate;
+  a.y_type = desc->y_dtype, a.u_type = desc->u_dtype, a.post_norm = desc->post_norm ? 1 : 0;
+  a.eps = desc->eps, a.alpha = desc->residual_scale, a.beta = desc->branch_scale;
+  const int sms = device_sm_count();
+  if (sms <= 0) return PI_ERR_CUDA;
+  const RowShape r = row_shape(a.d, 4 + (int)type_size(desc->y_dtype), false);
+  const dim3 g(tokens < sms * r.per_sm ? tokens : sms * r.per_sm);
+  cudaStream_t st = (cudaStream_t)stream;
+  switch (r.ch * 2 + r.rows) {
+  case 4:
+    return fwd_launch<1, 2>(a, g, r, st);
+  case 6:
+    return fwd_launch<2, 2>(a, g, r, st);
+  case 8:
+    return fwd_launch<3, 2>(a, g, r, st);
+  case 10:
+    return fwd_launch<4, 2>(a, g, r, st);
+  case 18:
+    return fwd_launch<8, 2>(a, g, r, st);
+  default:
+    return fwd_launch<8, 1>(a, g, r, st);
+  }
+}
+
+pi_status pi_block_norm_workspace_size(const pi_block_norm_desc *desc, int max_tokens, size_t *bytes) {
+  const pi_status s = check_norm(desc);
+  if (s != PI_OK) return s;
+  if (!bytes) return PI_ERR_INVALID_ARG;
+  if (max_tokens < 0 || max_tokens > kMaxTokens) return PI_ERR_UNSUPPORTED;
+  const int sms = device_sm_count();
+  if (sms <= 0) return PI_ERR_CUDA;
+  *bytes = norm_ws_bytes(desc->d_model, norm_bwd_blocks(kBwdBlocks, max_tokens, sms));
+  return PI_OK;
+}
+
+pi_status pi_block_norm_backward(const pi_block_norm_desc *desc, const float *x_out, const void *y,
+                                 const float *rstd_post, const float *rstd_pre, const void *du, const float *dx_out,
+                                 int tokens, float *dx, void *dy, float *dw_post, float *dw_pre, float *dgate,
+                                 unsigned flags, void *ws, size_t ws_bytes, pi_stream_t stream) {
+  pi_status s = check_norm(desc);
+  if (s != PI_OK) return s;
+  if (flags & ~(unsigned)PI_GRAD_ACCUMULATE) return PI_ERR_INVALID_ARG;
+  if ((dw_post && !desc->post_norm) || (dgate && !desc->gate)) return PI_ERR_INVALID_ARG;
+  if (tokens < 0 || tokens > kMaxTokens) return PI_ERR_UNSUPPORTED;
+  if (tokens) {
+    if (!du && !dx_out) return PI_ERR_INVALID_ARG;
+    if (du ? (!x_out || !rstd_pre) : dw_pre != nullptr) return PI_ERR_INVALID_ARG;
+    if (y ? (desc->post_norm && !rstd_post) : (dy || dw_post || dgate)) return PI_ERR_INVALID_ARG;
+  }
+  const void *ptrs[] = {x_out, y, rstd_post, rstd_pre, du, dx_out, dx, dy, dw_post, dw_pre, dgate};
+  for (const void *p : ptrs)
+    if (p && !aligned16(p)) return PI_ERR_MISALIGNED;
+  const int d = desc->d_model;
+  const size_t n = (size_t)tokens * d, nx = n * 4, ny = n * type_size(desc->y_dtype), nu = n * type_size(desc->u_dtype);
+  if ((dx != dx_out && overlap(dx, nx, dx_out, nx)) || overlap(dx, nx, x_out, nx) || overlap(dx, nx, y, ny) ||
+      overlap(dx, nx, du, nu) || overlap(dy, ny, x_out, nx) || (dy != y && overlap(dy, ny, y, ny)) ||
+      overlap(dy, ny, du, nu) || overlap(dy, ny, dx_out, nx) || overlap(dx, nx, dy, ny))
+    return PI_ERR_INVALID_ARG;
+  cudaStream_t st = (cudaStream_t)stream;
+  const int acc = (flags & PI_GRAD_ACCUMULATE) ? 1 : 0;
+  if (tokens == 0) {  // no tokens: the sums over them are zero (and there is no gate row)
+    if (!acc && dw_post) PI_CUDA(cudaMemsetAsync(dw_post, 0, (size_t)d * 4, st));
+    if (!acc && dw_pre) PI_CUDA(cudaMemsetAsync(dw_pre, 0, (size_t)d * 4, st));
+    return PI_OK;
+  }
+  if (!ws) return PI_ERR_WORKSPACE;
+  if (!aligned16(ws)) return PI_ERR_MISALIGNED;
+  const int sms = device_sm_count();
+  if (sms <= 0) return PI_ERR_CUDA;
+  const RowShape r = row_shape(d, 8 + (int)type_size(desc->u_dtype) + (int)type_size(desc->y_dtype), true);
+  const int G = norm_bwd_blocks(r.ch > 4 ? 1 : r.per_sm, tokens, sms);
+  if (ws_bytes < norm_ws_bytes(d, G)) return PI_ERR_WORKSPACE;
+  float *part = reinterpret_cast<float *>(static_cast<char *>(ws) + kHeader);
+  NM::BwdArgs a{};
+  a.x_out = x_out, a.y = y, a.du = du, a.rstd_post = rstd_post, a.rstd_pre = rstd_pre, a.dx_out = dx_out;
+  a.w_post = desc->w_post, a.w_pre = desc->w_pre, a.gate = desc->gate;
+  a.dx = dx, a.dy = dy, a.dgate = dgate;
+  a.part_post = dw_post ? part : nullptr;
+  a.part_pre = dw_pre ? part + (size_t)G * d : nullptr;
+  a.part_gate = part + (size_t)2 * G * d;
+  a.tokens = tokens, a.d = d, a.tokens_per_gate = desc->tokens_per_gate;
+  a.y_type = desc->y_dtype, a.u_type = desc->u_dtype, a.post_norm = desc->post_norm ? 1 : 0;
+  a.accumulate = acc;
+  a.alpha = desc->residual_scale, a.beta = desc->branch_scale;
+  switch (r.ch * 2 + r.rows) {
+  case 4:
+    s = bwd_launch<1, 2>(a, G, r, st);
+    break;
+  case 6:
+    s = bwd_launch<2, 2>(a, G, r, st);
+    break;
+  case 8:
+    s = bwd_launch<3, 2>(a, G, r, st);
+    break;
+  case 9:
+    s = bwd_launch<4, 1>(a, G, r, st);
+    break;
+  case 10:
+    s = bwd_launch<4, 2>(a, G, r, st);
+    break;
+  default: {
+    static DeviceOnce once;
+    PI_CUDA(launch1(NM::norm_bwd_wide_kernel, dim3(G), 1024, (size_t)d * 8, 0, &once, st, a));
+  }
+  }
+  if (s != PI_OK) return s;
+  if (dw_post || dw_pre || dgate) {
+    NM::JoinArgs j{};
+    j.part_post = a.part_post, j.part_pre = a.part_pre, j.part_gate = a.part_gate;
+    j.dw_post = dw_post, j.dw_pre = dw_pre, j.dgate = dgate;
+    j.G = G, j.tokens = tokens, j.d = d, j.tokens_per_gate = desc->tokens_per_gate, j.accumulate = acc;
+    const dim3 g(cdiv(d, 32), dgate ? 2 + NM::kGateJobs : 2);
+    PI_CUDA(launch1(NM::norm_join_kernel, g, 256, 0, 0, nullptr, st, j));
+  }
+  return PI_OK;
+}
+
+// ====================================================================== 8-bit quantiser
+pi_status pi_quantize_i8(const void *x, int x_dtype, int rows, int k, int8_t *q, float *scales, pi_stream_t stream) {
+  if (k <= 0 || !is_type(x_dtype)) return PI_ERR_INVALID_ARG;
+  if (k % 16 || rows < 0 || rows > kMaxTokens || k > kMaxI8K) return PI_ERR_UNSUPPORTED;
+  if (rows == 0) return PI_OK;
+  if (!x || !q || !scales) return PI_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(q) || !aligned16(scales)) return PI_ERR_MISALIGNED;
+  const int sms = device_sm_count();
+  if (sms <= 0) return PI_ERR_CUDA;
+  // a thread keeps up to 4 chunks of 8 elements; more threads for longer rows and for few rows
+  const int chunks = cdiv(k, 8);
+  const int most = rows < sms ? 1024 : 256;
+  int ch = cdiv(chunks, most);
+  ch = ch <= 1 ? 1 : ch <= 2 ? 2 : 4;
+  int threads = cdiv(cdiv(chunks, ch), 32) * 32;
+  if (threads > 1024) threads = 1024;
+  const int per_sm = 2048 / threads > 32 ? 32 : 2048 / threads;
+  const dim3 g(rows < sms * per_sm ? rows : sms * per_sm);
+  NM::QuantArgs a{x, q, scales, x_dtype, rows, k};
+  cudaStream_t st = (cudaStream_t)stream;
+  PI_CUDA(ch == 1   ? launch1(NM::quantize_i8_kernel<1>, g, threads, 0, 0, nullptr, st, a)
+         : ch == 2 ? launch1(NM::quantize_i8_kernel<2>, g, threads, 0, 0, nullptr, st, a)
+                   : launch1(NM::quantize_i8_kernel<4>, g, threads, 0, 0, nullptr, st, a));
+  return PI_OK;
+}
+
+}  // extern "C"

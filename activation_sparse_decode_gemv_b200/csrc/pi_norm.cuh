@@ -50,8 +50,8 @@ PI_DEV float dot4(float4 a, float4 b) { return fmaf(a.w, b.w, fmaf(a.z, b.z, fma
 PI_DEV float4 one4() { return make_float4(1.f, 1.f, 1.f, 1.f); }
 PI_DEV float4 zero4() { return make_float4(0.f, 0.f, 0.f, 0.f); }
 
-// Block-wide sums of N values; buf: 32 N floats of shared memory not in use
-// since the last barrier but one (callers alternate two buffers).
+// Block-wide sums of N values; buf: 32 N floats of shared memory that no warp
+// has read since the last but one barrier (callers alternate two buffers).
 template <int N>
 PI_DEV void block_sum(float (&v)[N], float *buf) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
@@ -65,6 +65,119 @@ PI_DEV void block_sum(float (&v)[N], float *buf) {
 #pragma unroll
   for (int k = 0; k < N; ++k) v[k] = warp_sum(lane < nw ? buf[k * 32 + lane] : 0.f);
 }
+
+// ---------------------------------------------------------------- four values as two packed pairs
+// fma.rn.f32x2 and its kin do two fp32 operations an instruction, each rounded
+// like the scalar one; the row kernels are short of issue slots, not of
+// arithmetic.
+struct P4 {
+  unsigned long long a, b;
+};
+PI_DEV unsigned long long pk(float lo, float hi) {
+  unsigned long long r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+PI_DEV unsigned long long fma2(unsigned long long x, unsigned long long y, unsigned long long z) {
+  unsigned long long r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
+  return r;
+}
+PI_DEV unsigned long long mul2(unsigned long long x, unsigned long long y) {
+  unsigned long long r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+  return r;
+}
+PI_DEV P4 fma(P4 x, P4 y, P4 z) { return P4{fma2(x.a, y.a, z.a), fma2(x.b, y.b, z.b)}; }
+PI_DEV P4 fma(unsigned long long s, P4 y, P4 z) { return P4{fma2(s, y.a, z.a), fma2(s, y.b, z.b)}; }
+PI_DEV P4 mul(P4 x, P4 y) { return P4{mul2(x.a, y.a), mul2(x.b, y.b)}; }
+PI_DEV P4 mul(unsigned long long s, P4 y) { return P4{mul2(s, y.a), mul2(s, y.b)}; }
+PI_DEV unsigned long long dot(P4 x, P4 y, unsigned long long z) { return fma2(x.b, y.b, fma2(x.a, y.a, z)); }
+PI_DEV float4 f4(P4 v) {
+  float4 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v.a));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.z), "=f"(r.w) : "l"(v.b));
+  return r;
+}
+PI_DEV P4 p4(float4 v) { return P4{pk(v.x, v.y), pk(v.z, v.w)}; }
+PI_DEV float sum2(unsigned long long v) {
+  float x, y;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
+  return x + y;
+}
+
+// ---------------------------------------------------------------- row ring
+// A thread owns the same 4-element chunks of every row (chunk tid + c *
+// blockDim of CH) and fetches them itself, by cp.async into slots of its own,
+// R rows ahead of their use.  No thread reads another's slot, so the ring
+// needs no barrier: cp.async.wait_group orders a thread's own copies.
+PI_DEV void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+PI_DEV void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+constexpr __host__ __device__ int chunk_bytes(int type) { return type == T_F32 ? 16 : 8; }
+
+// This thread's chunks of one row of a tensor: `step` = blockDim chunks apart.
+template <int CH, int TYPE>
+struct Part {
+  static constexpr int B = chunk_bytes(TYPE);
+  // row0: the tensor's row; valid: bit c set where chunk c lies inside it
+  static PI_DEV void fetch(uint32_t slot, const void *row0, int step, unsigned valid) {
+    const char *p = static_cast<const char *>(row0) + threadIdx.x * B;
+    slot += threadIdx.x * B;
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+      if (valid >> c & 1u) {
+        if constexpr (TYPE == T_F32)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(slot + c * step * B), "l"(p + c * step * B)
+                       : "memory");
+        else
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(slot + c * step * B), "l"(p + c * step * B)
+                       : "memory");
+      }
+  }
+  static PI_DEV P4 load(const unsigned char *slot, int c, int step) {
+    const unsigned char *p = slot + (threadIdx.x + c * step) * B;
+    if constexpr (TYPE == T_F32) {
+      const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(p);
+      return P4{v.x, v.y};
+    } else {
+      return p4(ld4(p, 0, TYPE));
+    }
+  }
+  static PI_DEV void store(void *row0, int c, int step, P4 v) {
+    char *p = static_cast<char *>(row0) + (threadIdx.x + c * step) * B;
+    if constexpr (TYPE == T_F32) *reinterpret_cast<ulonglong2 *>(p) = make_ulonglong2(v.a, v.b);
+    else st4(p, 0, TYPE, f4(v));
+  }
+  // slots that no copy fills read as zero
+  static PI_DEV void clear(unsigned char *slot, int step, unsigned valid) {
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+      if (!(valid >> c & 1u)) {
+        unsigned char *p = slot + (threadIdx.x + c * step) * B;
+        *reinterpret_cast<unsigned long long *>(p) = 0;
+        if (TYPE == T_F32) *reinterpret_cast<unsigned long long *>(p + 8) = 0;
+      }
+  }
+};
+template <int CH>
+PI_DEV unsigned valid_chunks(int d) {
+  unsigned v = 0;
+#pragma unroll
+  for (int c = 0; c < CH; ++c) v |= (unsigned)((int)(threadIdx.x + c * blockDim.x) * 4 < d) << c;
+  return v;
+}
+PI_DEV const void *row_at(const void *p, int t, int d, int type) {
+  return static_cast<const char *>(p) + (size_t)t * d * (type == T_F32 ? 4 : 2);
+}
+PI_DEV void *row_at(void *p, int t, int d, int type) {
+  return static_cast<char *>(p) + (size_t)t * d * (type == T_F32 ? 4 : 2);
+}
+
+// First of the rows that block c of G takes: contiguous runs of equal length.
+PI_DEV int first_token(int tokens, int G, int c) { return (int)((long long)tokens * c / G); }
 
 // ---------------------------------------------------------------- forward
 //   m = y rsqrt(mean y^2 + eps) (post_norm; else m = y),  b = m w_post
@@ -81,85 +194,137 @@ struct FwdArgs {
   float eps, alpha, beta;
 };
 
-// One block per row (grid-stride), CH chunks of 4 elements a thread, kept in
-// registers from the load to the store; two block sums a row.
-template <int CH>
-__global__ void __launch_bounds__(512) norm_fwd_kernel(const FwdArgs a) {
+// beta gate w_post of a chunk's columns
+PI_DEV float4 branch_factor(const float *gate_row, const float *w_post, float beta, int i) {
+  float4 f = make_float4(beta, beta, beta, beta);
+  if (w_post) f = mul4(f, ld4(w_post + i));
+  if (gate_row) f = mul4(f, ld4(gate_row + i));
+  return f;
+}
+
+// One block per run of rows; a row stays in registers between its two block
+// sums.  Bound by HBM: 4 + |y| bytes read and 4 + |u| written per element.
+// The column factors stay in registers too where they fit (CH <= 4).
+template <int CH, int R, int YT, int UT>
+__global__ void __launch_bounds__(512, CH <= 3 ? 2 : 1) norm_fwd_kernel(const FwdArgs a) {
+  constexpr bool KEEP = CH <= 4;
+  using X = Part<CH, T_F32>;
+  using Y = Part<CH, YT>;
+  using U = Part<CH, UT>;
+  extern __shared__ __align__(16) unsigned char ring[];
   __shared__ float buf[2][32];
+  const int d = a.d, step = blockDim.x, G = gridDim.x;
+  const int t0 = first_token(a.tokens, G, blockIdx.x), t1 = first_token(a.tokens, G, blockIdx.x + 1);
+  const float inv_d = 1.f / (float)d;
+  const unsigned valid = valid_chunks<CH>(d);
+  const int xb = CH * step * 16, slot_b = xb + CH * step * Y::B;
+  const uint32_t ring_s = (uint32_t)__cvta_generic_to_shared(ring);
+#pragma unroll
+  for (int k = 0; k < R; ++k) {
+    X::clear(ring + k * slot_b, step, valid);
+    Y::clear(ring + k * slot_b + xb, step, a.y ? valid : 0u);
+  }
+  auto fetch = [&](int t, int k) {  // row t into slot k
+    if (t < t1) {
+      X::fetch(ring_s + k * slot_b, row_at(a.x, t, d, T_F32), step, valid);
+      if (a.y) Y::fetch(ring_s + k * slot_b + xb, row_at(a.y, t, d, YT), step, valid);
+    }
+    cp_commit();
+  };
   pdl_wait();
   pdl_launch_dependents();
-  const float inv_d = 1.f / (float)a.d;
-  for (int t = blockIdx.x; t < a.tokens; t += gridDim.x) {
-    const size_t row = (size_t)t * a.d;
-    float4 r[CH], y[CH];
+#pragma unroll
+  for (int k = 0; k < R; ++k) fetch(t0 + k, k);
+  auto factor = [&](const float *gate_row, int c) {
+    return valid >> c & 1u ? p4(branch_factor(gate_row, a.w_post, a.beta, (threadIdx.x + c * step) * 4)) : p4(zero4());
+  };
+  auto weight = [&](int c) {
+    return a.w_pre && (valid >> c & 1u) ? p4(ld4(a.w_pre + (threadIdx.x + c * step) * 4)) : p4(one4());
+  };
+  int group = -1;
+  const float *gate_row = nullptr;
+  P4 bf[KEEP ? CH : 1], wp[KEEP ? CH : 1];
+  if constexpr (KEEP) {
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      const int i = (threadIdx.x + c * blockDim.x) * 4;
-      r[c] = y[c] = zero4();
-      if (i < a.d) {
-        r[c] = scale4(a.alpha, ld4(a.x + row + i));
-        if (a.y) y[c] = ld4(a.y, row + i, a.y_type);
+      wp[c] = weight(c);
+      if (!a.gate) bf[c] = factor(nullptr, c);
+    }
+  }
+  const unsigned long long alpha = pk(a.alpha, a.alpha);
+  int slot_i = 0;
+  for (int t = t0; t < t1; ++t) {
+    if (a.gate && t / a.tokens_per_gate != group) {
+      group = t / a.tokens_per_gate;
+      gate_row = a.gate + (size_t)group * d;
+      if constexpr (KEEP) {
+#pragma unroll
+        for (int c = 0; c < CH; ++c) bf[c] = factor(gate_row, c);
       }
     }
-    if (a.y) {
-      float k = a.beta;
-      if (a.post_norm) {
-        float s[1] = {0.f};
+    cp_wait<R - 1>();
+    const unsigned char *slot = ring + slot_i * slot_b;
+    P4 r[CH], y[CH];
+    unsigned long long q = 0;
 #pragma unroll
-        for (int c = 0; c < CH; ++c) s[0] += dot4(y[c], y[c]);
-        block_sum(s, buf[0]);
-        const float rp = rsqrtf(s[0] * inv_d + a.eps);
-        if (a.rstd_post && threadIdx.x == 0) a.rstd_post[t] = rp;
-#pragma unroll
-        for (int c = 0; c < CH; ++c) y[c] = scale4(rp, y[c]);
-      }
-      const float *g = a.gate ? a.gate + (size_t)(t / a.tokens_per_gate) * a.d : nullptr;
-#pragma unroll
-      for (int c = 0; c < CH; ++c) {
-        const int i = (threadIdx.x + c * blockDim.x) * 4;
-        if (i < a.d) {
-          float4 b = y[c];
-          if (a.w_post) b = mul4(b, ld4(a.w_post + i));
-          if (g) b = mul4(b, ld4(g + i));
-          r[c] = add4(r[c], scale4(k, b));
-        }
-      }
+    for (int c = 0; c < CH; ++c) {
+      r[c] = mul(alpha, X::load(slot, c, step));
+      y[c] = Y::load(slot + xb, c, step);
+      q = dot(y[c], y[c], q);
     }
-    if (a.x_out)
+    fetch(t + R, slot_i);
+    if (++slot_i == R) slot_i = 0;
+    float rp = 1.f;
+    if (a.post_norm) {
+      float s[1] = {sum2(q)};
+      block_sum(s, buf[0]);
+      rp = rsqrtf(s[0] * inv_d + a.eps);
+      if (a.rstd_post && threadIdx.x == 0) a.rstd_post[t] = rp;
+    }
+    const unsigned long long rp2 = pk(rp, rp);
+    q = 0;
 #pragma unroll
-      for (int c = 0; c < CH; ++c) {
-        const int i = (threadIdx.x + c * blockDim.x) * 4;
-        if (i < a.d) *reinterpret_cast<float4 *>(a.x_out + row + i) = r[c];
-      }
+    for (int c = 0; c < CH; ++c) {
+      P4 f;
+      if constexpr (KEEP) f = bf[c];
+      else f = factor(gate_row, c);
+      r[c] = fma(mul(rp2, y[c]), f, r[c]);
+      q = dot(r[c], r[c], q);
+    }
+    if (a.x_out) {
+      void *o = row_at(a.x_out, t, d, T_F32);
+#pragma unroll
+      for (int c = 0; c < CH; ++c)
+        if (valid >> c & 1u) X::store(o, c, step, r[c]);
+    }
     if (a.u) {
-      float s[1] = {0.f};
-#pragma unroll
-      for (int c = 0; c < CH; ++c) s[0] += dot4(r[c], r[c]);
+      float s[1] = {sum2(q)};
       block_sum(s, buf[1]);
       const float rr = rsqrtf(s[0] * inv_d + a.eps);
       if (a.rstd_pre && threadIdx.x == 0) a.rstd_pre[t] = rr;
+      const unsigned long long rr2 = pk(rr, rr);
+      void *o = row_at(a.u, t, d, UT);
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
-        const int i = (threadIdx.x + c * blockDim.x) * 4;
-        if (i < a.d) {
-          float4 o = scale4(rr, r[c]);
-          if (a.w_pre) o = mul4(o, ld4(a.w_pre + i));
-          st4(a.u, row + i, a.u_type, o);
-        }
+        P4 w;
+        if constexpr (KEEP) w = wp[c];
+        else w = weight(c);
+        if (valid >> c & 1u) U::store(o, c, step, mul(mul(rr2, r[c]), w));
       }
     }
-    if (!(a.y && a.post_norm && a.u)) __syncthreads();  // one buffer in use: keep rows apart
+    if (!(a.post_norm && a.u)) __syncthreads();  // one buffer in use: keep rows apart
   }
 }
 
 // ---------------------------------------------------------------- backward
-// With n = r rstd_pre, m = y rstd_post (or y), q = beta gate w_post m:
-//   dr = dx_out + rstd_pre (du w_pre - n c/d),      c = sum du w_pre n
-//   dx = alpha dr,  dgate += beta w_post m dr,  dw_pre += du n,
-//   dw_post += beta gate m dr
-//   dy = rstd_post (v - m e/d),  v = beta gate w_post dr,
-//   e = sum v m = sum q dx_out + rstd_pre (sum q du w_pre - c/d sum q n)
-// so one block sum of three values (c and two of e's parts) serves a row.
+// With n = r rstd_pre, m = y rstd_post (or y), f = beta gate w_post:
+//   dr = dx_out + rstd_pre (du w_pre - n c/d),   c = sum du w_pre n
+//   dx = alpha dr,   dw_pre += du n
+//   dy = rstd_post (f dr - m e/d) (post_norm; else f dr),   e = sum f m dr
+//      = sum f m dx_out + rstd_pre (sum f m du w_pre - c/d sum f m n)
+// so one block sum of three values (c and e's two parts) serves a row.  The
+// gate's and w_post's gradients share S = sum of m dr over the tokens of a gate
+// row: dgate = beta w_post S, and dw_post += beta gate S once per gate row.
 struct BwdArgs {
   const float *x_out;  // r
   const void *y, *du;  // y null: no branch; du null: no pre-norm
@@ -168,137 +333,247 @@ struct BwdArgs {
   float *dx;
   void *dy;
   float *dgate;
-  float *part_post, *part_pre;  // [G x d] column sums of a block's rows
+  float *part_post, *part_pre;  // [G x d] column sums of a block's rows (null: not wanted)
   float *part_gate;             // [G x 2 x d] of its first and last gate rows, where shared with other blocks
   int tokens, d, tokens_per_gate;
   int y_type, u_type, post_norm, accumulate;
   float alpha, beta;
 };
 
-PI_DEV int first_token(int tokens, int G, int c) { return (int)((long long)tokens * c / G); }
-
-// One block per contiguous run of rows; column sums stay in registers and are
-// written once per block (per gate row for dgate), so their order is fixed.
-template <int CH>
-__global__ void __launch_bounds__(512) norm_bwd_kernel(const BwdArgs a) {
-  __shared__ float buf[2][96];
-  pdl_wait();
-  pdl_launch_dependents();
-  const int G = gridDim.x, cta = blockIdx.x;
-  const int t0 = first_token(a.tokens, G, cta), t1 = first_token(a.tokens, G, cta + 1);
-  const float inv_d = 1.f / (float)a.d;
-  const bool want_gate = a.dgate != nullptr;
-  float4 s_pre[CH], s_post[CH], s_gate[CH];
-#pragma unroll
-  for (int c = 0; c < CH; ++c) s_pre[c] = s_post[c] = s_gate[c] = zero4();
-  int group = a.gate ? t0 / a.tokens_per_gate : 0;
-  const int group0 = group;
-
-  auto flush_gate = [&]() {
+// At the end of the tokens of gate row `group` (or of the block's rows): adds
+// beta gate S to the block's dw_post sums and stores the gate's gradient, for
+// the 4 columns at i.  post0: nothing is in part_post yet.
+PI_DEV void flush_gate(const BwdArgs &a, int group, int group0, int t0, int t1, int i, float4 S, bool post0) {
+  const float *grow = a.gate ? a.gate + (size_t)group * a.d : nullptr;
+  if (a.part_post) {
+    float4 v = scale4(a.beta, S);
+    if (grow) v = mul4(v, ld4(grow + i));
+    float *dst = a.part_post + (size_t)blockIdx.x * a.d + i;
+    if (!post0) v = add4(v, ld4(dst));
+    *reinterpret_cast<float4 *>(dst) = v;
+  }
+  if (a.dgate) {
     // a gate row used by this block alone is finished here; a shared one goes to the joining kernel
     const long long g0 = (long long)group * a.tokens_per_gate;
     const long long g1 = min((long long)a.tokens, g0 + a.tokens_per_gate);
     const bool whole = g0 >= t0 && g1 <= t1;
-    float *dst = whole ? a.dgate + (size_t)group * a.d : a.part_gate + ((size_t)cta * 2 + (group != group0)) * a.d;
-#pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      const int i = (threadIdx.x + c * blockDim.x) * 4;
-      if (i < a.d) {
-        float4 v = s_gate[c];
-        if (whole && a.accumulate) v = add4(v, ld4(dst + i));
-        *reinterpret_cast<float4 *>(dst + i) = v;
-      }
-      s_gate[c] = zero4();
-    }
-  };
-
-  for (int t = t0; t < t1; ++t) {
-    const size_t row = (size_t)t * a.d;
-    if (a.gate) {
-      const int gi = t / a.tokens_per_gate;
-      if (gi != group) {
-        if (want_gate) flush_gate();
-        group = gi;
-      }
-    }
-    const float *g = a.gate ? a.gate + (size_t)group * a.d : nullptr;
-    const float rr = a.du ? a.rstd_pre[t] : 0.f;
-    const float rp = a.y && a.post_norm ? a.rstd_post[t] : 1.f;
-    float4 n[CH], v[CH], m[CH], dr[CH];
-    float s[3] = {0.f, 0.f, 0.f};
-#pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      const int i = (threadIdx.x + c * blockDim.x) * 4;
-      n[c] = v[c] = m[c] = dr[c] = zero4();
-      if (i < a.d) {
-        if (a.dx_out) dr[c] = ld4(a.dx_out + row + i);
-        if (a.du) {
-          n[c] = scale4(rr, ld4(a.x_out + row + i));
-          v[c] = ld4(a.du, row + i, a.u_type);
-        }
-        if (a.y) m[c] = scale4(rp, ld4(a.y, row + i, a.y_type));
-      }
-    }
-#pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      const int i = (threadIdx.x + c * blockDim.x) * 4;
-      if (i < a.d) {
-        if (a.du) {
-          s_pre[c] = add4(s_pre[c], mul4(v[c], n[c]));
-          if (a.w_pre) v[c] = mul4(v[c], ld4(a.w_pre + i));
-          s[0] += dot4(v[c], n[c]);
-          // dr without the term of c
-          dr[c] = add4(dr[c], scale4(rr, v[c]));
-        }
-        if (a.y && a.post_norm) {
-          float4 q = scale4(a.beta, m[c]);
-          if (g) q = mul4(q, ld4(g + i));
-          if (a.w_post) q = mul4(q, ld4(a.w_post + i));
-          s[1] += dot4(q, dr[c]);
-          s[2] += dot4(q, n[c]);
-        }
-      }
-    }
-    block_sum(s, buf[t & 1]);
-    const float cd = rr * s[0] * inv_d;           // dr -= cd n
-    const float ed = (s[1] - cd * s[2]) * inv_d;  // dy = rp (v - m ed)
-#pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      const int i = (threadIdx.x + c * blockDim.x) * 4;
-      if (i < a.d) {
-        const float4 d4 = add4(dr[c], scale4(-cd, n[c]));
-        if (a.dx) *reinterpret_cast<float4 *>(a.dx + row + i) = scale4(a.alpha, d4);
-        if (a.y) {
-          float4 b = scale4(a.beta, d4);  // gradient of gate * w_post * m
-          const float4 w = a.w_post ? ld4(a.w_post + i) : one4();
-          if (want_gate) s_gate[c] = add4(s_gate[c], mul4(b, mul4(w, m[c])));
-          if (g) b = mul4(b, ld4(g + i));
-          if (a.post_norm) {
-            s_post[c] = add4(s_post[c], mul4(b, m[c]));
-            b = scale4(rp, add4(mul4(b, w), scale4(-ed, m[c])));
-          } else {
-            b = mul4(b, w);
-          }
-          if (a.dy) st4(a.dy, row + i, a.y_type, b);
-        }
-      }
-    }
-  }
-  if (want_gate && t1 > t0) flush_gate();
-#pragma unroll
-  for (int c = 0; c < CH; ++c) {
-    const int i = (threadIdx.x + c * blockDim.x) * 4;
-    if (i < a.d) {
-      if (a.part_post) *reinterpret_cast<float4 *>(a.part_post + (size_t)cta * a.d + i) = s_post[c];
-      if (a.part_pre) *reinterpret_cast<float4 *>(a.part_pre + (size_t)cta * a.d + i) = s_pre[c];
-    }
+    float4 v = scale4(a.beta, S);
+    if (a.w_post) v = mul4(v, ld4(a.w_post + i));
+    float *dst = (whole ? a.dgate + (size_t)group * a.d
+                        : a.part_gate + ((size_t)blockIdx.x * 2 + (group != group0)) * a.d) + i;
+    if (whole && a.accumulate) v = add4(v, ld4(dst));
+    *reinterpret_cast<float4 *>(dst) = v;
   }
 }
 
-// Joins the blocks' column sums in block order.  blockIdx.y: 0 dw_post, 1
-// dw_pre, 2 + b: the gate row that crosses from block b's rows into block
-// b + 1's, taken once, by the first boundary inside it.  A block sums 32
-// columns, 8 partial rows at a time.
+// One block per run of rows (CH <= 4 chunks a thread).  Column sums stay in
+// registers, dw_post's in the block's own row of partials, so every order is
+// fixed.  A tensor that is not given has zeros in its part of the ring.
+template <int CH, int R, int YT, int UT>
+__global__ void __launch_bounds__(512) norm_bwd_kernel(const BwdArgs a) {
+  using X = Part<CH, T_F32>;
+  using Y = Part<CH, YT>;
+  using U = Part<CH, UT>;
+  extern __shared__ __align__(16) unsigned char ring[];
+  __shared__ float buf[2][96];
+  const int d = a.d, step = blockDim.x, G = gridDim.x;
+  const int t0 = first_token(a.tokens, G, blockIdx.x), t1 = first_token(a.tokens, G, blockIdx.x + 1);
+  const float inv_d = 1.f / (float)d;
+  const unsigned valid = valid_chunks<CH>(d);
+  const int o_g = CH * step * 16, o_u = 2 * o_g, o_y = o_u + CH * step * U::B, slot_b = o_y + CH * step * Y::B;
+  const uint32_t ring_s = (uint32_t)__cvta_generic_to_shared(ring);
+#pragma unroll
+  for (int k = 0; k < R; ++k) {
+    unsigned char *slot = ring + k * slot_b;
+    X::clear(slot, step, a.du ? valid : 0u);
+    X::clear(slot + o_g, step, a.dx_out ? valid : 0u);
+    U::clear(slot + o_u, step, a.du ? valid : 0u);
+    Y::clear(slot + o_y, step, a.y ? valid : 0u);
+  }
+  auto fetch = [&](int t, int k) {  // row t into slot k
+    if (t < t1) {
+      const uint32_t slot = ring_s + k * slot_b;
+      if (a.du) {
+        X::fetch(slot, row_at(a.x_out, t, d, T_F32), step, valid);
+        U::fetch(slot + o_u, row_at(a.du, t, d, UT), step, valid);
+      }
+      if (a.dx_out) X::fetch(slot + o_g, row_at(a.dx_out, t, d, T_F32), step, valid);
+      if (a.y) Y::fetch(slot + o_y, row_at(a.y, t, d, YT), step, valid);
+    }
+    cp_commit();
+  };
+  pdl_wait();
+  pdl_launch_dependents();
+#pragma unroll
+  for (int k = 0; k < R; ++k) fetch(t0 + k, k);
+  const bool post = a.y && a.post_norm;
+  auto rr_of = [&](int t) { return a.du ? __ldg(a.rstd_pre + t) : 0.f; };
+  auto rp_of = [&](int t) { return post ? __ldg(a.rstd_post + t) : 1.f; };
+  auto factor = [&](const float *gate_row, int c) {
+    return valid >> c & 1u ? p4(branch_factor(gate_row, a.w_post, a.beta, (threadIdx.x + c * step) * 4)) : p4(zero4());
+  };
+  P4 s_pre[CH], S[CH], bf[CH];
+  int group = a.gate ? t0 / a.tokens_per_gate : 0;
+  const int group0 = group;
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    s_pre[c] = S[c] = p4(zero4());
+    bf[c] = factor(a.gate ? a.gate + (size_t)group * d : nullptr, c);
+  }
+  bool post0 = true;  // part_post is empty
+  auto flush = [&]() {
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      if (valid >> c & 1u) flush_gate(a, group, group0, t0, t1, (threadIdx.x + c * step) * 4, f4(S[c]), post0);
+      S[c] = p4(zero4());
+    }
+    post0 = false;
+  };
+  const unsigned long long alpha = pk(a.alpha, a.alpha);
+  float rr_next = rr_of(t0), rp_next = rp_of(t0);
+  int slot_i = 0;
+  for (int t = t0; t < t1; ++t) {
+    if (a.gate) {
+      const int gi = t / a.tokens_per_gate;
+      if (gi != group) {
+        flush();
+        group = gi;
+#pragma unroll
+        for (int c = 0; c < CH; ++c) bf[c] = factor(a.gate + (size_t)group * d, c);
+      }
+    }
+    const float rr = rr_next, rp = rp_next;
+    if (t + 1 < t1) rr_next = rr_of(t + 1), rp_next = rp_of(t + 1);
+    const unsigned long long rr2 = pk(rr, rr), rp2 = pk(rp, rp);
+    cp_wait<R - 1>();
+    const unsigned char *slot = ring + slot_i * slot_b;
+    P4 n[CH], m[CH], dr[CH];
+    unsigned long long q0 = 0, q1 = 0, q2 = 0;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      n[c] = mul(rr2, X::load(slot, c, step));
+      m[c] = mul(rp2, Y::load(slot + o_y, c, step));
+      P4 v = U::load(slot + o_u, c, step);
+      s_pre[c] = fma(v, n[c], s_pre[c]);
+      if (a.w_pre && (valid >> c & 1u)) v = mul(v, p4(ld4(a.w_pre + (threadIdx.x + c * step) * 4)));
+      q0 = dot(v, n[c], q0);
+      dr[c] = fma(rr2, v, X::load(slot + o_g, c, step));  // dr without the term of c
+      const P4 q = mul(bf[c], m[c]);
+      q1 = dot(q, dr[c], q1);
+      q2 = dot(q, n[c], q2);
+    }
+    fetch(t + R, slot_i);
+    if (++slot_i == R) slot_i = 0;
+    float s[3] = {sum2(q0), sum2(q1), sum2(q2)};
+    block_sum(s, buf[t & 1]);
+    const float cd = rr * s[0] * inv_d;                         // dr -= cd n
+    const float ed = post ? (s[1] - cd * s[2]) * inv_d : 0.f;   // dy = rp (f dr - ed m)
+    const unsigned long long cd2 = pk(-cd, -cd), ed2 = pk(-ed, -ed);
+    void *dx = a.dx ? row_at(a.dx, t, d, T_F32) : nullptr, *dy = a.dy ? row_at(a.dy, t, d, YT) : nullptr;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const P4 d4 = fma(cd2, n[c], dr[c]);
+      S[c] = fma(m[c], d4, S[c]);
+      const P4 b = mul(rp2, fma(ed2, m[c], mul(bf[c], d4)));
+      if (valid >> c & 1u) {
+        if (dx) X::store(dx, c, step, mul(alpha, d4));
+        if (dy) Y::store(dy, c, step, b);
+      }
+    }
+  }
+  if (a.y && (a.part_post || a.dgate)) flush();
+#pragma unroll
+  for (int c = 0; c < CH; ++c)
+    if (a.part_pre && (valid >> c & 1u))
+      *reinterpret_cast<float4 *>(a.part_pre + (size_t)blockIdx.x * d + (threadIdx.x + c * step) * 4) = f4(s_pre[c]);
+}
+
+// The same for rows whose values and column sums exceed the registers (d >
+// 8192): a row is read twice, the second time from L2, and the column sums
+// live in shared memory ([2 x d]: dw_pre's and S).
+__global__ void __launch_bounds__(1024) norm_bwd_wide_kernel(const BwdArgs a) {
+  extern __shared__ __align__(16) unsigned char ring[];
+  __shared__ float buf[2][96];
+  pdl_wait();
+  pdl_launch_dependents();
+  float *s_pre = reinterpret_cast<float *>(ring), *S = s_pre + a.d;
+  const int G = gridDim.x;
+  const int t0 = first_token(a.tokens, G, blockIdx.x), t1 = first_token(a.tokens, G, blockIdx.x + 1);
+  const float inv_d = 1.f / (float)a.d;
+  const int step = blockDim.x * 4, i0 = threadIdx.x * 4;
+  for (int i = i0; i < a.d; i += step) {
+    *reinterpret_cast<float4 *>(s_pre + i) = zero4();
+    *reinterpret_cast<float4 *>(S + i) = zero4();
+  }
+  int group = a.gate ? t0 / a.tokens_per_gate : 0;
+  const int group0 = group;
+  bool post0 = true;
+  auto flush = [&]() {
+    for (int i = i0; i < a.d; i += step) {
+      flush_gate(a, group, group0, t0, t1, i, ld4(S + i), post0);
+      *reinterpret_cast<float4 *>(S + i) = zero4();
+    }
+    post0 = false;
+  };
+  for (int t = t0; t < t1; ++t) {
+    const size_t row = (size_t)t * a.d;
+    if (a.gate && t / a.tokens_per_gate != group) {
+      flush();
+      group = t / a.tokens_per_gate;
+    }
+    const float *grow = a.gate ? a.gate + (size_t)group * a.d : nullptr;
+    const float rr = a.du ? a.rstd_pre[t] : 0.f;
+    const float rp = a.y && a.post_norm ? a.rstd_post[t] : 1.f;
+    auto load = [&](int i, float4 &n, float4 &v, float4 &m, float4 &dr) {
+      n = v = m = dr = zero4();
+      if (a.dx_out) dr = ld4(a.dx_out + row + i);
+      if (a.y) m = scale4(rp, ld4(a.y, row + i, a.y_type));
+      if (a.du) {
+        n = scale4(rr, ld4(a.x_out + row + i));
+        v = ld4(a.du, row + i, a.u_type);
+      }
+    };
+    float s[3] = {0.f, 0.f, 0.f};
+#pragma unroll 2
+    for (int i = i0; i < a.d; i += step) {
+      float4 n, v, m, dr;
+      load(i, n, v, m, dr);
+      if (a.w_pre) v = mul4(v, ld4(a.w_pre + i));
+      s[0] += dot4(v, n);
+      const float4 q = mul4(branch_factor(grow, a.w_post, a.beta, i), m);
+      s[1] += dot4(q, add4(dr, scale4(rr, v)));
+      s[2] += dot4(q, n);
+    }
+    block_sum(s, buf[t & 1]);
+    const float cd = rr * s[0] * inv_d;
+    const float ed = a.post_norm ? (s[1] - cd * s[2]) * inv_d : 0.f;
+#pragma unroll 2
+    for (int i = i0; i < a.d; i += step) {
+      float4 n, v, m, dr;
+      load(i, n, v, m, dr);
+      float4 *sp = reinterpret_cast<float4 *>(s_pre + i), *sg = reinterpret_cast<float4 *>(S + i);
+      *sp = add4(*sp, mul4(v, n));
+      if (a.w_pre) v = mul4(v, ld4(a.w_pre + i));
+      const float4 d4 = add4(add4(dr, scale4(rr, v)), scale4(-cd, n));
+      const float4 f = branch_factor(grow, a.w_post, a.beta, i);
+      *sg = add4(*sg, mul4(m, d4));
+      // a row's inputs are read before its outputs are written, element by element: dx may be dx_out, dy y
+      if (a.dx) *reinterpret_cast<float4 *>(a.dx + row + i) = scale4(a.alpha, d4);
+      if (a.dy) st4(a.dy, row + i, a.y_type, scale4(rp, add4(mul4(f, d4), scale4(-ed, m))));
+    }
+  }
+  if (a.y && (a.part_post || a.dgate)) flush();
+  if (a.part_pre)
+    for (int i = i0; i < a.d; i += step)
+      *reinterpret_cast<float4 *>(a.part_pre + (size_t)blockIdx.x * a.d + i) = ld4(s_pre + i);
+}
+
+// Joins the blocks' column sums in block order, 32 columns a block.
+// blockIdx.y: 0 dw_post, 1 dw_pre, 2.. the gate rows that cross from one
+// block's rows into the next's.  Such a row is taken by the first boundary
+// inside it; boundaries are dealt round robin over kGateJobs blocks.
+constexpr int kGateJobs = 16;
+constexpr int kMaxBwdBlocks = 2048;
 struct JoinArgs {
   const float *part_post, *part_pre, *part_gate;
   float *dw_post, *dw_pre, *dgate;
@@ -308,40 +583,71 @@ __global__ void __launch_bounds__(256) norm_join_kernel(const JoinArgs a) {
   pdl_wait();
   pdl_launch_dependents();
   __shared__ float buf[8][32];
+  __shared__ int first[kMaxBwdBlocks + 1];  // the blocks' first tokens
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int i = blockIdx.x * 32 + lane;
+  const bool in = i < a.d;
   const int job = blockIdx.y;
-  int c0 = 0, c1 = a.G;  // blocks whose partials are summed
-  float *out = job == 0 ? a.dw_post : a.dw_pre;
-  const float *part = job == 0 ? a.part_post : a.part_pre;
-  long long g0 = 0;
   if (job >= 2) {
-    const int b = job - 2;
-    const int cut = first_token(a.tokens, a.G, b + 1);
-    const int group = cut / a.tokens_per_gate;
-    g0 = (long long)group * a.tokens_per_gate;
-    if (g0 == cut || first_token(a.tokens, a.G, b) > g0) return;  // no crossing, or an earlier boundary has it
-    const long long g1 = min((long long)a.tokens, g0 + a.tokens_per_gate);
-    c0 = b;
-    for (c1 = b + 1; c1 < a.G && first_token(a.tokens, a.G, c1) < g1;) ++c1;
-    out = a.dgate ? a.dgate + (size_t)group * a.d : nullptr;
-    part = a.part_gate;
+    for (int c = threadIdx.x; c <= a.G; c += 256) first[c] = first_token(a.tokens, a.G, c);
+    __syncthreads();
   }
-  if (!out) return;
-  float s = 0.f;
-  if (i < a.d)
-    for (int c = c0 + w; c < c1; c += 8) {
-      size_t row = c;
-      if (job >= 2)  // the block's first gate row is in its slot 0, another in slot 1
-        row = (size_t)c * 2 + (first_token(a.tokens, a.G, c) < g0 ? 1 : 0);
-      s += part[row * a.d + i];
+  auto put = [&](float *out, float s) { *out = a.accumulate ? *out + s : s; };
+  if (job < 2) {
+    float *out = job == 0 ? a.dw_post : a.dw_pre;
+    const float *part = job == 0 ? a.part_post : a.part_pre;
+    if (!out) return;
+    float s = 0.f;
+    if (in) {
+#pragma unroll 8
+      for (int c = w; c < a.G; c += 8) s += part[(size_t)c * a.d + i];
     }
-  buf[w][lane] = s;
-  __syncthreads();
-  if (w == 0 && i < a.d) {
+    buf[w][lane] = s;
+    __syncthreads();
+    if (w == 0 && in) {
 #pragma unroll
-    for (int k = 1; k < 8; ++k) s += buf[k][lane];
-    out[i] = a.accumulate ? out[i] + s : s;
+      for (int k = 1; k < 8; ++k) s += buf[k][lane];
+      put(out + i, s);
+    }
+    return;
+  }
+  // the shared gate row at boundary b (between blocks b and b + 1): its blocks c0..c1-1, false if another boundary has it
+  int group, c1, slot_b;
+  auto shared_row = [&](int b) {
+    const int cut = first[b + 1];
+    group = cut / a.tokens_per_gate;
+    const int g0 = group * a.tokens_per_gate;
+    if (g0 == cut || first[b] > g0) return false;
+    const long long g1 = min((long long)a.tokens, (long long)g0 + a.tokens_per_gate);
+    c1 = min(a.G, (int)((g1 * a.G + a.tokens - 1) / a.tokens));  // blocks whose first token is below g1
+    slot_b = first[b] < g0 ? 1 : 0;
+    return true;
+  };
+  // a block's first gate row is in its slot 0, another in slot 1: only the first block can have begun before the row
+  auto part_of = [&](int c, int b) { return a.part_gate[((size_t)c * 2 + (c == b ? slot_b : 0)) * a.d + i]; };
+  // rows shared by up to 8 blocks: a warp each
+  for (int b = (job - 2) + kGateJobs * w; b < a.G - 1; b += kGateJobs * 8) {
+    if (!shared_row(b) || c1 - b > 8 || !in) continue;
+    float s = part_of(b, b);
+    for (int c = b + 1; c < c1; ++c) s += part_of(c, b);
+    put(a.dgate + (size_t)group * a.d + i, s);
+  }
+  // longer ones: all warps
+  for (int b = job - 2; b < a.G - 1; b += kGateJobs) {
+    if (!shared_row(b) || c1 - b <= 8) continue;
+    float s = 0.f;
+    if (in) {
+#pragma unroll 4
+      for (int c = b + w; c < c1; c += 8) s += part_of(c, b);
+    }
+    __syncthreads();
+    buf[w][lane] = s;
+    __syncthreads();
+    if (w == 0 && in) {
+#pragma unroll
+      for (int k = 1; k < 8; ++k) s += buf[k][lane];
+      put(a.dgate + (size_t)group * a.d + i, s);
+    }
   }
 }
 
@@ -350,9 +656,22 @@ __global__ void __launch_bounds__(256) norm_join_kernel(const JoinArgs a) {
 // even).  A row of zeros has scale 0 and codes 0; a row that holds an
 // infinity or a NaN has scale NaN and codes 0, so its products are NaN.
 PI_DEV void ld8(const void *p, size_t i, int type, float (&v)[8]) {
-  const float4 a = ld4(p, i, type), b = ld4(p, i + 4, type);
+  float4 a, b;
+  if (type == T_F32) {
+    a = ld4(p, i, type), b = ld4(p, i + 4, type);
+  } else {
+    const uint4 w = *reinterpret_cast<const uint4 *>(reinterpret_cast<const uint16_t *>(p) + i);
+    const uint2 h[2] = {make_uint2(w.x, w.y), make_uint2(w.z, w.w)};
+    a = ld4(h, 0, type), b = ld4(h, 4, type);
+  }
   v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
 }
+struct QuantArgs {
+  const void *x;
+  int8_t *q;
+  float *scales;
+  int type, rows, k;
+};
 PI_DEV uint32_t code4(const float *v, float scale) {
   uint32_t w = 0;
 #pragma unroll
@@ -362,40 +681,60 @@ PI_DEV uint32_t code4(const float *v, float scale) {
   }
   return w;
 }
-__global__ void __launch_bounds__(1024) quantize_i8_kernel(const void *__restrict__ x, int type, int rows, int k,
-                                                          int8_t *__restrict__ q, float *__restrict__ scales) {
+// One block per row; CH chunks of 8 elements a thread, all loads in flight
+// together and kept as loaded until they are coded.  Rows longer than CH
+// chunks a block (k > 32768) are read again from L2.
+template <int CH>
+__global__ void __launch_bounds__(1024) quantize_i8_kernel(const QuantArgs a) {
   __shared__ unsigned buf[2][32];
   pdl_wait();
   pdl_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
-  for (int r = blockIdx.x, it = 0; r < rows; r += gridDim.x, ++it) {
-    const size_t row = (size_t)r * k;
+  const int step = blockDim.x * 8;
+  for (int r = blockIdx.x, it = 0; r < a.rows; r += gridDim.x, ++it) {
+    const size_t row = (size_t)r * a.k;
     unsigned amax = 0;  // bits of |x|: they order like the values, and a NaN above all
-    float v0[8];
-    for (int i = threadIdx.x * 8; i < k; i += blockDim.x * 8) {
-      float v[8];
-      ld8(x, row + i, type, v);
+    float v[CH][8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) amax = max(amax, __float_as_uint(v[j]) & 0x7fffffffu);
-      if (i == (int)threadIdx.x * 8)
+    for (int c = 0; c < CH; ++c) {
+      const int i = threadIdx.x * 8 + c * step;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v0[j] = v[j];
+      for (int j = 0; j < 8; ++j) v[c][j] = 0.f;
+      if (i < a.k) ld8(a.x, row + i, a.type, v[c]);
+    }
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) amax = max(amax, __float_as_uint(v[c][j]) & 0x7fffffffu);
+    for (int i = threadIdx.x * 8 + CH * step; i < a.k; i += step) {
+      float t[8];
+      ld8(a.x, row + i, a.type, t);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) amax = max(amax, __float_as_uint(t[j]) & 0x7fffffffu);
     }
     amax = __reduce_max_sync(0xffffffffu, amax);
-    if (lane == 0) buf[it & 1][warp] = amax;
-    __syncthreads();
-    amax = __reduce_max_sync(0xffffffffu, lane < nw ? buf[it & 1][lane] : 0u);
+    if (nw > 1) {
+      if (lane == 0) buf[it & 1][warp] = amax;
+      __syncthreads();
+      amax = __reduce_max_sync(0xffffffffu, lane < nw ? buf[it & 1][lane] : 0u);
+    }
     const bool bad = amax >= 0x7f800000u;
     const float scale = bad ? __uint_as_float(0x7fffffffu) : __fdiv_rn(__uint_as_float(amax), 127.f);
-    if (threadIdx.x == 0) scales[r] = scale;
+    if (threadIdx.x == 0) a.scales[r] = scale;
     const bool zero = bad || scale == 0.f;
-    for (int i = threadIdx.x * 8; i < k; i += blockDim.x * 8) {
-      uint2 w = make_uint2(0u, 0u);
-      if (!zero) {
-        if (i != (int)threadIdx.x * 8) ld8(x, row + i, type, v0);
-        w = make_uint2(code4(v0, scale), code4(v0 + 4, scale));
-      }
-      *reinterpret_cast<uint2 *>(q + row + i) = w;
+    auto put = [&](int i, const float (&t)[8]) {
+      *reinterpret_cast<uint2 *>(a.q + row + i) =
+          zero ? make_uint2(0u, 0u) : make_uint2(code4(t, scale), code4(t + 4, scale));
+    };
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int i = threadIdx.x * 8 + c * step;
+      if (i < a.k) put(i, v[c]);
+    }
+    for (int i = threadIdx.x * 8 + CH * step; i < a.k; i += step) {
+      float t[8];
+      ld8(a.x, row + i, a.type, t);
+      put(i, t);
     }
   }
 }
