@@ -320,24 +320,49 @@ def pi_get_device_status(ws: torch.Tensor, stream=None) -> int:
 
 
 # ---------------------------------------------------------------- dense block operators
+# These calls serve single tokens too, where a call's host time is what the
+# user waits for, so the checks make one pass over the tensors.
 def _check_out(t: Optional[torch.Tensor], what: str, dtype, shape):
     """An exactly shaped contiguous tensor (None passes)."""
     if t is None:
         return
     if t.dtype != dtype:
         raise ValueError(f"{what}: dtype {t.dtype}, expected {dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{what}: must be contiguous")
 
 
-def _one_device(**tensors: Optional[torch.Tensor]):
-    """All tensors on the current CUDA device: kernels launch there, on its current stream."""
-    _on_device(**tensors)
-    for what, t in tensors.items():
-        if t is not None and t.device.index != torch.cuda.current_device():
-            raise ValueError(f"{what}: on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
+def _ptrs(names: str, *tensors: Optional[torch.Tensor]):
+    """The tensors' addresses (None stays None).  All of them on the current
+    CUDA device: kernels launch there, on its current stream."""
+    dev = -2
+    out = []
+    for k, t in enumerate(tensors):
+        if t is None:
+            out.append(None)
+            continue
+        d = t.get_device()
+        if d != dev:
+            what = names.split()[k]
+            if d < 0:
+                raise ValueError(f"{what}: must be a CUDA tensor")
+            if d != torch.cuda.current_device():
+                raise ValueError(f"{what}: on {t.device}, but the current device is "
+                                 f"cuda:{torch.cuda.current_device()}")
+            dev = d
+        out.append(t.data_ptr())
+    return out
+
+
+def _raw_stream(stream):
+    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+
+
+def _ws_bytes(ws: torch.Tensor) -> int:
+    _need_ws(ws)
+    return ws.numel() * ws.element_size()
 
 
 def _zeroed_workspace(n: int, device=None) -> torch.Tensor:
@@ -400,10 +425,10 @@ def pi_gated_ffn_forward(layer: GatedFfnLayer, u: torch.Tensor, y: torch.Tensor,
     _check_out(y, "y", layer.dtype, (T, layer.d))
     _check_out(gate, "gate", layer.dtype, (T, layer.f))
     _check_out(up, "up", layer.dtype, (T, layer.f))
-    _need_ws(ws)
-    _one_device(u=u, y=y, gate=gate, up=up, workspace=ws, weights=layer._keep[0])
-    _check(lib().pi_gated_ffn_forward(layer.handle, _p(u), T, _p(y), _p(gate), _p(up), *_wsargs(ws),
-                                      _stream(stream)), "pi_gated_ffn_forward")
+    n = _ws_bytes(ws)
+    pu, py, pg, pp, pw, _ = _ptrs("u y gate up workspace weights", u, y, gate, up, ws, layer._keep[0])
+    _check(lib().pi_gated_ffn_forward(layer.handle, pu, T, py, pg, pp, pw, n, _raw_stream(stream)),
+           "pi_gated_ffn_forward")
 
 
 def pi_gated_ffn_backward(layer: GatedFfnLayer, u: torch.Tensor, gate: torch.Tensor, up: torch.Tensor,
@@ -422,12 +447,11 @@ def pi_gated_ffn_backward(layer: GatedFfnLayer, u: torch.Tensor, gate: torch.Ten
         raise ValueError(f"dw_*: dtype {gtype}, expected torch.float32 or {layer.dtype}")
     for what, t in (("dw_gate", dw_gate), ("dw_up", dw_up), ("dw_down_t", dw_down_t)):
         _check_out(t, what, gtype, (layer.f, layer.d))
-    _need_ws(ws)
-    _one_device(u=u, gate=gate, up=up, dy=dy, du=du, dw_gate=dw_gate, dw_up=dw_up, dw_down_t=dw_down_t, workspace=ws,
-                weights=layer._keep[0])
-    _check(lib().pi_gated_ffn_backward(layer.handle, _p(u), _p(gate), _p(up), _p(dy), T, _p(du), _p(dw_gate),
-                                       _p(dw_up), _p(dw_down_t), DTYPE[gtype], int(flags), *_wsargs(ws),
-                                       _stream(stream)), "pi_gated_ffn_backward")
+    n = _ws_bytes(ws)
+    pu, pg, pp, pdy, pdu, p0, p1, p2, pw, _ = _ptrs("u gate up dy du dw_gate dw_up dw_down_t workspace weights", u,
+                                                    gate, up, dy, du, dw_gate, dw_up, dw_down_t, ws, layer._keep[0])
+    _check(lib().pi_gated_ffn_backward(layer.handle, pu, pg, pp, pdy, T, pdu, p0, p1, p2, DTYPE[gtype], int(flags),
+                                       pw, n, _raw_stream(stream)), "pi_gated_ffn_backward")
 
 
 class BlockNorm:
@@ -453,6 +477,7 @@ class BlockNorm:
         self.w_post, self.w_pre = w_post, w_pre
         self.desc = pi_block_norm_desc(d, DTYPE[y_dtype], DTYPE[u_dtype], int(post_norm), eps, residual_scale,
                                        branch_scale, _p(w_post), _p(w_pre), _p(gate), int(tokens_per_gate))
+        self.ref = C.byref(self.desc)
 
     def _check_tokens(self, T: int):
         """The gate has a row for each of T tokens."""
@@ -474,15 +499,15 @@ def pi_block_norm_forward(norm: BlockNorm, x: torch.Tensor, y: Optional[torch.Te
     _check_out(u, "u", norm.u_dtype, (T, norm.d))
     _check_out(rstd_post, "rstd_post", torch.float32, (T,))
     _check_out(rstd_pre, "rstd_pre", torch.float32, (T,))
-    _one_device(x=x, y=y, x_out=x_out, u=u, rstd_post=rstd_post, rstd_pre=rstd_pre, w_post=norm.w_post,
-                w_pre=norm.w_pre, gate=norm.gate)
-    _check(lib().pi_block_norm_forward(C.byref(norm.desc), _p(x), _p(y), T, _p(x_out), _p(u), _p(rstd_post),
-                                       _p(rstd_pre), _stream(stream)), "pi_block_norm_forward")
+    px, py, po, pu, pk, pr, *_ = _ptrs("x y x_out u rstd_post rstd_pre w_post w_pre gate", x, y, x_out, u, rstd_post,
+                                       rstd_pre, norm.w_post, norm.w_pre, norm.gate)
+    _check(lib().pi_block_norm_forward(norm.ref, px, py, T, po, pu, pk, pr, _raw_stream(stream)),
+           "pi_block_norm_forward")
 
 
 def pi_block_norm_workspace_size(norm: BlockNorm, max_tokens: int) -> int:
     n = C.c_size_t()
-    _check(lib().pi_block_norm_workspace_size(C.byref(norm.desc), int(max_tokens), C.byref(n)),
+    _check(lib().pi_block_norm_workspace_size(norm.ref, int(max_tokens), C.byref(n)),
            "pi_block_norm_workspace_size")
     return n.value
 
@@ -517,13 +542,12 @@ def pi_block_norm_backward(norm: BlockNorm, x_out: Optional[torch.Tensor], y: Op
         if norm.gate is None:
             raise ValueError("dgate: there is no gate")
         _check_out(dgate, "dgate", torch.float32, norm.gate.shape)
-    _need_ws(ws)
-    _one_device(x_out=x_out, y=y, rstd_post=rstd_post, rstd_pre=rstd_pre, du=du, dx_out=dx_out, dx=dx, dy=dy,
-                workspace=ws, dw_post=dw_post, dw_pre=dw_pre, dgate=dgate, w_post=norm.w_post, w_pre=norm.w_pre,
-                gate=norm.gate)
-    _check(lib().pi_block_norm_backward(C.byref(norm.desc), _p(x_out), _p(y), _p(rstd_post), _p(rstd_pre), _p(du),
-                                        _p(dx_out), T, _p(dx), _p(dy), _p(dw_post), _p(dw_pre), _p(dgate),
-                                        int(flags), *_wsargs(ws), _stream(stream)), "pi_block_norm_backward")
+    n = _ws_bytes(ws)
+    (pr, py, pkp, pkr, pdu, pg, pdx, pdy, pw, p0, p1, p2, *_) = _ptrs(
+        "x_out y rstd_post rstd_pre du dx_out dx dy workspace dw_post dw_pre dgate w_post w_pre gate", x_out, y,
+        rstd_post, rstd_pre, du, dx_out, dx, dy, ws, dw_post, dw_pre, dgate, norm.w_post, norm.w_pre, norm.gate)
+    _check(lib().pi_block_norm_backward(norm.ref, pr, py, pkp, pkr, pdu, pg, T, pdx, pdy, p0, p1, p2, int(flags), pw,
+                                        n, _raw_stream(stream)), "pi_block_norm_backward")
 
 
 def pi_quantize_i8(x: torch.Tensor, q: torch.Tensor, scales: torch.Tensor, stream=None):
@@ -534,9 +558,8 @@ def pi_quantize_i8(x: torch.Tensor, q: torch.Tensor, scales: torch.Tensor, strea
     _check_out(x, "x", x.dtype, (rows, k))
     _check_out(q, "q", torch.int8, (rows, k))
     _check_out(scales, "scales", torch.float32, (rows,))
-    _one_device(x=x, q=q, scales=scales)
-    _check(lib().pi_quantize_i8(_p(x), DTYPE[x.dtype], rows, k, _p(q), _p(scales), _stream(stream)),
-           "pi_quantize_i8")
+    px, pq, ps = _ptrs("x q scales", x, q, scales)
+    _check(lib().pi_quantize_i8(px, DTYPE[x.dtype], rows, k, pq, ps, _raw_stream(stream)), "pi_quantize_i8")
 
 
 def pi_matmul_i8_workspace_size(tokens: int, n: int, k: int) -> int:
@@ -566,7 +589,8 @@ def pi_matmul_i8(xq: torch.Tensor, x_scales: torch.Tensor, wq: torch.Tensor, w_s
     _check_out(w_scales, "w_scales", torch.float32, (n,))
     _check_out(bias, "bias", torch.float32, (n,))
     _check_out(y, "y", y.dtype, (T, n))
-    _need_ws(ws)
-    _one_device(xq=xq, x_scales=x_scales, wq=wq, w_scales=w_scales, bias=bias, y=y, workspace=ws)
-    _check(lib().pi_matmul_i8(_p(xq), _p(x_scales), _p(wq), _p(w_scales), _p(bias), T, n, k, _p(y), DTYPE[y.dtype],
-                              *_wsargs(ws), _stream(stream)), "pi_matmul_i8")
+    size = _ws_bytes(ws)
+    pq, ps, pwq, pws, pb_, py, pw = _ptrs("xq x_scales wq w_scales bias y workspace", xq, x_scales, wq, w_scales, bias,
+                                          y, ws)
+    _check(lib().pi_matmul_i8(pq, ps, pwq, pws, pb_, T, n, k, py, DTYPE[y.dtype], pw, size, _raw_stream(stream)),
+           "pi_matmul_i8")

@@ -4,6 +4,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 #include <new>
 
@@ -27,27 +28,91 @@ namespace GM = pi::gemm;
 
 constexpr int kMaxI8K = 131056;        // 128 * 128 * K stays below 2^31
 constexpr int kMaxDim = 1 << 20;
+constexpr int kMaxSplit = 8;  // CTAs of a cluster
 
 template <int EPI, int AMN, int BMN, int MB, int NT, typename T>
 cudaError_t pair_launch(const GM::Args &a, int sms, cudaStream_t st) {
   static DeviceOnce once;
+  GM::Args b = a;
+  // The side with fewer tiles is swept for each step along the other, so that
+  // the larger operand is read once and the smaller stays in L2: forward of
+  // 2048 x 8192 x 28672 2160 us with m sweeps of 1, 2185 of 4, 2215 of 8, 2470 of
+  // 16; backward of 4096 x 5120 x 13824 2710, 2658, 2624 (its dW: 10 x 54 tiles).
+  // Sweeps of more than 24 tiles would not stay in L2.
+  b.gm = (a.mt <= a.nt ? a.mt : a.nt) > 24 ? 8 : a.mt <= a.nt ? a.mt : 1;
   const long long tiles = (long long)a.nprob * a.mt * a.nt;
   const int pairs = (int)(tiles < sms / 2 ? tiles : sms / 2);
   return launch1(GM::pair_gemm_kernel<EPI, AMN, BMN, MB, NT, T>, dim3(2 * pairs), GM::kPairThreads,
-                 GM::PairShape<EPI, MB, NT>::SMEM, 0, &once, st, a, GM::PairShape<EPI, MB, NT>::SMEM);
+                 GM::PairShape<EPI, MB, NT>::SMEM, 0, &once, st, b, GM::PairShape<EPI, MB, NT>::SMEM);
 }
-template <int EPI, int AMN, int NT, typename T>
-cudaError_t split_launch(const GM::Args &a, int split, cudaStream_t st) {
+// Clusters of `split` CTAs with the split kernel's shape that the device holds
+// at once (cached per device).  Asked for an empty kernel: for one that
+// allocates tensor memory the occupancy calculator answers with one CTA per
+// SM, whatever it allocates, but the hardware runs two.
+__global__ void __launch_bounds__(GM::kSplitThreads) shape_kernel() {}
+template <int NT>
+int resident_clusters(int split) {
   static DeviceOnce once;
-  return launch1(GM::split_gemm_kernel<EPI, AMN, NT, T>, dim3((unsigned)(a.mt * a.nt * split)), GM::kSplitThreads,
-                 GM::SplitShape<NT>::SMEM, split, &once, st, a, GM::SplitShape<NT>::SMEM);
+  static std::atomic<int> cache[64][kMaxSplit + 1];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  int n = cache[dev][split].load(std::memory_order_relaxed);
+  if (n == 0) {
+    if (once.ensure([] {
+          const cudaError_t e =
+              cudaFuncSetAttribute(shape_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+          return e != cudaSuccess ? e
+                                  : cudaFuncSetAttribute(shape_kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                                         cudaSharedmemCarveoutMaxShared);
+        }) != cudaSuccess)
+      return 0;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(split);
+    cfg.blockDim = dim3(GM::kSplitThreads);
+    cfg.dynamicSmemBytes = GM::SplitShape<NT>::SMEM;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = (unsigned)split;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, shape_kernel, &cfg) != cudaSuccess) {
+      cudaGetLastError();
+      return 0;
+    }
+    cache[dev][split].store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
+// The largest split whose clusters all run at once, at least 4 K blocks each:
+// a second round of clusters would double the time (one token, 5120 x 13824:
+// down product split by 6 70.5 us for the block, by 7 (more clusters than fit)
+// 83.8, by 4 74.3, by 2 97.9).
+template <int EPI, int AMN, int NT, typename T>
+cudaError_t split_launch(const GM::Args &a, cudaStream_t st) {
+  static DeviceOnce once;
+  const auto kern = GM::split_gemm_kernel<EPI, AMN, NT, T>;
+  cudaError_t e = once.ensure([&] {
+    // an SM's memory as shared memory: two CTAs are resident
+    cudaError_t r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, GM::SplitShape<NT>::SMEM);
+    return r != cudaSuccess ? r
+                            : cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                                   cudaSharedmemCarveoutMaxShared);
+  });
+  if (e != cudaSuccess) return e;
+  const int tiles = a.mt * a.nt;
+  int split = a.kb / 4 < kMaxSplit ? a.kb / 4 : kMaxSplit;
+  while (split > 1 && resident_clusters<NT>(split) < tiles) --split;
+  if (split < 1) split = 1;
+  return launch1(kern, dim3((unsigned)(tiles * split)), GM::kSplitThreads,
+                 GM::SplitShape<NT>::SMEM, split, nullptr, st, a);
 }
 
 // How a product runs.  nt: token columns of a tile; mb: 256-feature blocks of
-// a CTA-pair tile; split: 0 = CTA-pair kernel, else the cluster size that K is
-// split over.
+// a CTA-pair tile; split: the split-K kernel instead.
 struct Plan {
-  int nt, mb, split;
+  int nt, mb;
+  bool split;
   int b_rows() const { return split ? nt : nt / 2; }  // rows of the B box
 };
 
@@ -64,22 +129,16 @@ double pair_cost(long long tiles, int pairs, int kb, int mb, int nt) {
 Plan choose(int m, int m_rows, int n, int kb, int sms, int max_mb, bool nt192) {
   Plan p{};
   p.mb = 1;
-  auto split_of = [&](int tiles) {
-    int s = 1;
-    while (s < 8 && tiles * s < sms && kb >= 4 * s) s *= 2;
-    return s;
-  };
-  const int mt = cdiv(m, m_rows);
   if (n <= 128) {
     p.nt = n <= 16 ? 16 : n <= 32 ? 32 : n <= 64 ? 64 : 128;
-    p.split = split_of(mt);
+    p.split = true;
     return p;
   }
   const int pairs = sms / 2;
   const int pair_tiles = cdiv(m, 2 * m_rows) * cdiv(n, 128);
   if (pair_tiles < pairs / 2) {
     p.nt = 128;
-    p.split = split_of(mt * cdiv(n, 128));
+    p.split = true;
     return p;
   }
   double best = 0;
@@ -104,10 +163,10 @@ cudaError_t run_plan(GM::Args &a, const Plan &p, int dtype, int m_rows, int sms,
   a.nt = cdiv(a.n, p.nt);
   a.idesc = idesc(dtype, EPI == GM::E_I8, p.split ? 128 : 256, p.nt, AMN, 0);
   if (!p.split) {
-    if constexpr (EPI != GM::E_DGLU) {
+    if constexpr (EPI == GM::E_STORE || EPI == GM::E_GLU) {
       if (p.mb == 2 && p.nt == 256) return pair_launch<EPI, AMN, 0, 2, 256, T>(a, sms, st);
     }
-    if constexpr (EPI == GM::E_STORE || EPI == GM::E_I8) {
+    if constexpr (EPI == GM::E_STORE) {
       if (p.mb == 2) return pair_launch<EPI, AMN, 0, 2, 192, T>(a, sms, st);
     }
     return p.nt == 256 ? pair_launch<EPI, AMN, 0, 1, 256, T>(a, sms, st)
@@ -115,13 +174,13 @@ cudaError_t run_plan(GM::Args &a, const Plan &p, int dtype, int m_rows, int sms,
   }
   switch (p.nt) {
   case 16:
-    return split_launch<EPI, AMN, 16, T>(a, p.split, st);
+    return split_launch<EPI, AMN, 16, T>(a, st);
   case 32:
-    return split_launch<EPI, AMN, 32, T>(a, p.split, st);
+    return split_launch<EPI, AMN, 32, T>(a, st);
   case 64:
-    return split_launch<EPI, AMN, 64, T>(a, p.split, st);
+    return split_launch<EPI, AMN, 64, T>(a, st);
   default:
-    return split_launch<EPI, AMN, 128, T>(a, p.split, st);
+    return split_launch<EPI, AMN, 128, T>(a, st);
   }
 }
 
@@ -371,7 +430,9 @@ pi_status pi_matmul_i8(const int8_t *xq, const float *x_scales, const int8_t *wq
   GM::Args a{};
   a.m = n, a.n = tokens, a.nprob = 1;
   a.kb = a.kb_seg = cdiv(k, 128);
-  const Plan p = choose(n, 128, tokens, a.kb, sms, 2, true);
+  // pair tiles of one block: the scaling epilogue costs more than the B reads that two save (2011 x
+  // 5120 x 13824: 126 against 135 us)
+  const Plan p = choose(n, 128, tokens, a.kb, sms, 1, false);
   if (!map_2d(&a.ma[0], wq, false, (uint64_t)k, (uint64_t)n, 128, 128, true) ||
       !map_2d(&a.mb[0], xq, false, (uint64_t)k, (uint64_t)tokens, 128, (uint32_t)p.b_rows(), true))
     return PI_ERR_CUDA;

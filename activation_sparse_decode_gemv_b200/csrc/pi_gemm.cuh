@@ -55,6 +55,7 @@ struct Args {
   int kb, kb_seg;    // K blocks per tile; per segment (kb = kb_seg x segments)
   int nprob;         // independent products of the same shape (1 segment each)
   int mt, nt;        // tiles along m and n
+  int gm;            // m tiles walked together (CTA-pair kernel)
   uint32_t idesc;    // MMA instruction descriptor
   void *out[kMaxMaps];
   long long ldo;     // elements between consecutive n of out, gate_*, up_*
@@ -84,9 +85,9 @@ PI_DEV void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-PI_DEV float ld_cluster_f32(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+PI_DEV float2 ld_cluster_f32x2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
   return v;
 }
 PI_DEV void mbar_arrive_cluster(uint32_t cluster_addr) {
@@ -200,18 +201,25 @@ template <> struct Elem<__nv_bfloat16> {
 };
 
 // ---------------------------------------------------------------- gate activations
-// phi and phi' in fp32; the caller rounds once.  The approximate exponential
-// and quotient (about 2^-21 relative) stay far below that rounding.
+// phi and phi' in fp32; the caller rounds once.  e^-g = 2^(-g log2 e) and the
+// reciprocal are the hardware's approximations (about 2^-22 relative, more by
+// |g| 2^-24 from the exponent's rounding), far below that rounding.
+PI_DEV float sigmoid(float g) {
+  float t, s;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(g * -1.44269504f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.f + t));
+  return s;
+}
 template <int ACT>
 PI_DEV float gate_phi(float g) {
-  if constexpr (ACT == G_SILU) return __fdividef(g, 1.f + __expf(-g));
+  if constexpr (ACT == G_SILU) return g * sigmoid(g);
   if constexpr (ACT == G_RELU) return g < 0.f ? 0.f : g;  // NaN stays NaN
   return 0.5f * g * (1.f + erff(g * 0.70710678f));
 }
 template <int ACT>
 PI_DEV void gate_phi_grad(float g, float &phi, float &slope) {
   if constexpr (ACT == G_SILU) {
-    const float s = __fdividef(1.f, 1.f + __expf(-g));
+    const float s = sigmoid(g);
     phi = g * s;
     slope = s * (1.f + g * (1.f - s));
   } else if constexpr (ACT == G_RELU) {
@@ -265,7 +273,8 @@ PI_DEV bool whole_piece(const Args &a, int m, int n0) {
 
 template <int NC, typename T>
 PI_DEV void put_t(const Args &a, void *out, int m, int n0, bool ok, const float (&v)[NC]) {
-  if constexpr (NC % 2 == 0) {
+  static_assert(NC % 2 == 0, "whole words");
+  {
     if (whole_piece<NC>(a, m, n0)) {
       char *p = reinterpret_cast<char *>(reinterpret_cast<T *>(out) + (size_t)(n0 + (threadIdx.x & 1)) * a.ldo + (m & ~1));
       const long long step = 4 * a.ldo;
@@ -315,36 +324,64 @@ PI_DEV void put_cols(const Args &a, void *out, int m, int n0, bool ok, float (&v
   }
 }
 
+// features m, m + 1 (m even) of token n
+template <typename T>
+PI_DEV void put_row2(const Args &a, void *out, int m, int n, const float (&v)[2]) {
+  if (m >= a.m) return;
+  T *p = reinterpret_cast<T *>(out) + (size_t)n * a.ldo + m;
+  if constexpr (__is_same(T, float)) {
+    p[0] = v[0];
+    if (m + 1 < a.m) p[1] = v[1];
+  } else {
+    if ((a.ldo & 1) == 0) {  // a.m is even too: ldo is the row length
+      *reinterpret_cast<uint32_t *>(p) = pack2<T>(v[0], v[1]);
+    } else {
+      p[0] = Elem<T>::from(v[0]);
+      if (m + 1 < a.m) p[1] = Elem<T>::from(v[1]);
+    }
+  }
+}
+
 template <int NC>
 PI_DEV void epi_i8(const Args &a, int m, int n0, bool ok, const float (&v)[NC]) {
   const float sm = ok ? __ldg(a.s_m + m) : 0.f;
   const float b = ok && a.bias ? __ldg(a.bias + m) : 0.f;
-  float o[NC];
+  float o[NC], sn[NC];
+  if (NC % 4 == 0 && n0 + NC <= a.n) {
 #pragma unroll
-  for (int j = 0; j < NC; ++j) {
-    const float sn = __ldg(a.s_n + min(n0 + j, a.n - 1));
-    o[j] = fmaf((float)__float_as_int(v[j]) * sn, sm, b);
+    for (int j = 0; j + 3 < NC; j += 4) {
+      const float4 f = __ldg(reinterpret_cast<const float4 *>(a.s_n + n0 + j));
+      sn[j] = f.x, sn[j + 1] = f.y, sn[j + 2] = f.z, sn[j + 3] = f.w;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < NC; ++j) sn[j] = __ldg(a.s_n + min(n0 + j, a.n - 1));
   }
+#pragma unroll
+  for (int j = 0; j < NC; ++j) o[j] = fmaf((float)__float_as_int(v[j]) * sn[j], sm, b);
   if (a.out_type == O_F32) put_f32<NC>(a, a.out[0], m, n0, ok, o);
   else if (a.out_type == O_F16) put_t<NC, __half>(a, a.out[0], m, n0, ok, o);
   else put_t<NC, __nv_bfloat16>(a, a.out[0], m, n0, ok, o);
 }
 
-template <int NC, typename T, int ACT>
-PI_DEV void epi_dglu_act(const Args &a, int m, int n0, bool ok, const float (&v)[NC], const float (&g)[NC],
-                         const float (&p)[NC]) {
-  float dg[NC], dp[NC], av[NC];
+template <int NC, int ACT>
+PI_DEV void dglu_act(const float (&da)[NC], const float (&g)[NC], const float (&p)[NC], float (&dg)[NC],
+                     float (&dp)[NC], float (&av)[NC]) {
 #pragma unroll
   for (int j = 0; j < NC; ++j) {
     float phi, slope;
     gate_phi_grad<ACT>(g[j], phi, slope);
-    dp[j] = v[j] * phi;
-    dg[j] = v[j] * p[j] * slope;
+    dp[j] = da[j] * phi;
+    dg[j] = da[j] * p[j] * slope;
     av[j] = phi * p[j];
   }
-  put_t<NC, T>(a, a.gate_out, m, n0, ok, dg);
-  put_t<NC, T>(a, a.up_out, m, n0, ok, dp);
-  put_t<NC, T>(a, a.out[0], m, n0, ok, av);
+}
+template <int NC>
+PI_DEV void dglu(int act, const float (&da)[NC], const float (&g)[NC], const float (&p)[NC], float (&dg)[NC],
+                 float (&dp)[NC], float (&av)[NC]) {
+  if (act == G_SILU) dglu_act<NC, G_SILU>(da, g, p, dg, dp, av);
+  else if (act == G_RELU) dglu_act<NC, G_RELU>(da, g, p, dg, dp, av);
+  else dglu_act<NC, G_GELU>(da, g, p, dg, dp, av);
 }
 // NC columns of a 16-bit matrix, as words of two columns of this lane's feature; zero outside
 template <int NC, typename T>
@@ -385,14 +422,6 @@ PI_DEV void load_gp(const Args &a, int m, int n0, bool ok, float (&g)[NC], float
     if (j + 1 < NC) p[j + 1] = y;
   }
 }
-template <int NC, typename T>
-PI_DEV void epi_dglu(const Args &a, int m, int n0, bool ok, const float (&v)[NC], const float (&g)[NC],
-                     const float (&p)[NC]) {
-  if (a.act == G_SILU) epi_dglu_act<NC, T, G_SILU>(a, m, n0, ok, v, g, p);
-  else if (a.act == G_RELU) epi_dglu_act<NC, T, G_RELU>(a, m, n0, ok, v, g, p);
-  else epi_dglu_act<NC, T, G_GELU>(a, m, n0, ok, v, g, p);
-}
-
 template <int NC>
 PI_DEV void glu(int act, const float (&g)[NC], const float (&p)[NC], float (&o)[NC]) {
   if (act == G_SILU) {
@@ -431,7 +460,7 @@ PI_DEV void load_a(const Args &a, int map, int blk, int row0, uint32_t dst, Load
 }
 
 // ================================================================ CTA-pair kernel
-constexpr int kPairThreads = 384;  // producer, MMA issuer, L2 prefetcher, idle warp, 8 epilogue warps
+constexpr int kPairThreads = 320;  // producer, MMA issuer, 8 epilogue warps
 constexpr int kPairEpi = 8;
 constexpr int kLead = 2;           // MB = 2: K blocks that one accumulator block runs ahead of the other
 
@@ -464,11 +493,11 @@ struct Ctrl {
 struct TileAt {
   int prob, m, n;  // tile indices
 };
-// Groups of 8 m tiles walked together over all n tiles: the tiles in flight
-// on the machine form a block of about 8 x 9, so each operand row is read
-// from HBM a few times and from L2 otherwise.
+// Groups of gm m tiles walked together over all n tiles: the tiles in flight
+// on the machine form a block of about gm x 74/gm, so each operand row is read
+// from HBM once or twice and from L2 otherwise.
 PI_DEV TileAt tile_at(const Args &a, int t) {
-  constexpr int GM = 8;
+  const int GM = a.gm;
   const int per = a.mt * a.nt;
   TileAt r;
   r.prob = t / per;
@@ -510,7 +539,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     C.abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 2) tmem_alloc_pair(&C.tmem, S::TMEM_COLS);
+  if (warp == 1) tmem_alloc_pair(&C.tmem, S::TMEM_COLS);
   tc_fence_before();
   __syncthreads();
   cluster_sync();
@@ -534,6 +563,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       for (int t = pair; t < tiles && ok; t += npairs) {
         const TileAt at = tile_at(a, t);
         const int col0 = at.n * NT + rank * S::NB;
+        if constexpr (EPI == E_DGLU) {
+          // the tile's g and p into L2, one main loop ahead of the epilogue
+          // that reads them (from HBM those reads left 783 TFLOP/s, from L2 1150)
+#pragma unroll
+          for (int b = 0; b < MB; ++b) {
+            const int row0 = ((at.m * MB + b) * 2 + rank) * MROWS;
+            if (row0 >= a.m) continue;
+            prefetch_l2_2d(&a.ma[1], row0, at.n * NT);
+            prefetch_l2_2d(&a.ma[2], row0, at.n * NT);
+          }
+        }
         for (int kb = 0; kb < a.kb; ++kb) {
           if (it >= S::NS && !mbar_wait_cluster(&C.empty[s], ph ^ 1u, abort_flag, a.status)) {
             ok = false;
@@ -632,26 +672,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       }
     }
     __syncwarp();
-  } else if (warp == 2) {
-    // ------------------------------------------------------------ E_DGLU: brings the next tile's g and p into L2
-    if (EPI == E_DGLU && lane == 0) {
-      int tc = -1;
-      for (int t = pair; t < tiles; t += npairs, ++tc) {
-        if (tc >= 0 && !mbar_wait_cluster(&C.accfull[buf_of(tc, MB - 1)], par_of(tc), abort_flag, a.status)) break;
-        const TileAt at = tile_at(a, t);
-#pragma unroll
-        for (int b = 0; b < MB; ++b) {
-          const int row0 = ((at.m * MB + b) * 2 + rank) * MROWS;
-          if (row0 >= a.m) continue;
-          prefetch_l2_2d(&a.ma[1], row0, at.n * NT);
-          prefetch_l2_2d(&a.ma[2], row0, at.n * NT);
-        }
-      }
-    }
-    __syncwarp();
-  } else if (warp >= 4) {
+  } else {
     // ------------------------------------------------------------ epilogue: lane quarter q, column half h
-    const int q = warp & 3, h = (warp - 4) >> 2;
+    const int q = warp & 3, h = (warp - 2) >> 2;
     const int lrow = q * 32 + lane;  // row of this CTA's half block
     int tc = 0;
     bool go = true;
@@ -719,7 +742,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
               float g[16], p[16];
               load_gp<16, T>(a, m, nc, in, g, p);
               tmem_ld16(tbase + c * 16, v);
-              epi_dglu<16, T>(a, m, nc, in, v, g, p);
+              float dg[16], dp[16], av[16];
+              dglu<16>(a.act, v, g, p, dg, dp, av);
+              put_t<16, T>(a, a.gate_out, m, nc, in, dg);
+              put_t<16, T>(a, a.up_out, m, nc, in, dp);
+              put_t<16, T>(a, a.out[0], m, nc, in, av);
             } else {
               tmem_ld16(tbase + c * 16, v);
               if constexpr (EPI == E_I8) epi_i8<16>(a, m, nc, in, v);
@@ -738,7 +765,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   __syncthreads();
   cluster_sync();
   tc_fence_after();
-  if (warp == 2) tmem_dealloc_pair(tmem, S::TMEM_COLS);
+  if (warp == 1) tmem_dealloc_pair(tmem, S::TMEM_COLS);
 }
 
 // ================================================================ split-K kernel
@@ -806,6 +833,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2) split_gemm_kernel(const __gr
       const int early = a.early_a ? min(S::NS, k1 - k0) : 0;
       for (int i = 0; i < early; ++i) start_a(k0 + i, i);
       pdl_wait();
+      pdl_launch_dependents();  // after the wait: the next kernel may rely on everything before this one
       for (int kb = k0; kb < k1; ++kb) {
         const int i = kb - k0, s = i % S::NS;
         const unsigned ph = (unsigned)((i / S::NS) & 1);
@@ -861,46 +889,70 @@ __global__ void __launch_bounds__(kSplitThreads, 2) split_gemm_kernel(const __gr
   tc_fence_before();
   __syncthreads();
   cluster_sync();  // every CTA's partial tile is in its shared memory
-  pdl_launch_dependents();
   {
     // ------------------------------------------------------------ join: this CTA's slice of the tile, summed in rank order
+    // (two features of a token at a time)
     const int nv = min(NT, a.n - col0);
     const int E = nv * MROWS;
-    const int per = ((E + split * 32 - 1) / (split * 32)) * 32;
+    const int per = ((E + split * 64 - 1) / (split * 64)) * 64;
     const int e0 = rank * per, e1 = min(E, e0 + per);
     const uint32_t red = su32(smem);
-    for (int e = e0 + tid; e < e1; e += kSplitThreads) {
+    for (int e = e0 + 2 * tid; e < e1; e += 2 * kSplitThreads) {
       const int n = e / MROWS, r = e % MROWS;
       const uint32_t off = red + (uint32_t)(n * 128 + r) * 4;
       const int m = row0 + r;
-      const bool in = m < a.m;
-      float v[1], w[1] = {0.f};
+      float v[2] = {0.f, 0.f}, w[2] = {0.f, 0.f};
       if constexpr (I8) {
-        int sum = 0;
-#pragma unroll 4
-        for (int c = 0; c < split; ++c) sum += __float_as_int(ld_cluster_f32(mapa(off, c)));
-        v[0] = __int_as_float(sum);
-        epi_i8<1>(a, m, col0 + n, in, v);
-      } else {
-        v[0] = 0.f;
+        int s0 = 0, s1 = 0;
 #pragma unroll 4
         for (int c = 0; c < split; ++c) {
-          v[0] += ld_cluster_f32(mapa(off, c));
-          if constexpr (EPI == E_GLU) w[0] += ld_cluster_f32(mapa(off + 256, c));
+          const float2 f = ld_cluster_f32x2(mapa(off, c));
+          s0 += __float_as_int(f.x), s1 += __float_as_int(f.y);
         }
-        if constexpr (EPI == E_GLU) {
-          float o[1];
-          glu<1>(a.act, v, w, o);
-          if (a.gate_out) put_t<1, T>(a, a.gate_out, m, col0 + n, in, v);
-          if (a.up_out) put_t<1, T>(a, a.up_out, m, col0 + n, in, w);
-          put_t<1, T>(a, a.out[0], m, col0 + n, in, o);
-        } else if constexpr (EPI == E_DGLU) {
-          float g[1], p[1];
-          load_gp<1, T>(a, m, col0 + n, in, g, p);
-          epi_dglu<1, T>(a, m, col0 + n, in, v, g, p);
-        } else {
-          put_cols<1, T>(a, a.out[0], m, col0 + n, in, v, a.out_type, a.accumulate);
+        v[0] = __int_as_float(s0), v[1] = __int_as_float(s1);
+      } else {
+#pragma unroll 4
+        for (int c = 0; c < split; ++c) {
+          const float2 f = ld_cluster_f32x2(mapa(off, c));
+          v[0] += f.x, v[1] += f.y;
+          if constexpr (EPI == E_GLU) {
+            const float2 g = ld_cluster_f32x2(mapa(off + 256, c));
+            w[0] += g.x, w[1] += g.y;
+          }
         }
+      }
+      if constexpr (EPI == E_GLU) {
+        float o[2];
+        glu<2>(a.act, v, w, o);
+        if (a.gate_out) put_row2<T>(a, a.gate_out, m, col0 + n, v);
+        if (a.up_out) put_row2<T>(a, a.up_out, m, col0 + n, w);
+        put_row2<T>(a, a.out[0], m, col0 + n, o);
+      } else if constexpr (EPI == E_I8) {
+        const float sn = __ldg(a.s_n + col0 + n);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int mj = min(m + j, a.m - 1);
+          v[j] = fmaf((float)__float_as_int(v[j]) * sn, __ldg(a.s_m + mj), a.bias ? __ldg(a.bias + mj) : 0.f);
+        }
+        if (a.out_type == O_F32) put_row2<float>(a, a.out[0], m, col0 + n, v);
+        else if (a.out_type == O_F16) put_row2<__half>(a, a.out[0], m, col0 + n, v);
+        else put_row2<__nv_bfloat16>(a, a.out[0], m, col0 + n, v);
+      } else if constexpr (EPI == E_DGLU) {
+        // features come in pairs (f is a multiple of 8)
+        float dg[2] = {0.f, 0.f}, dp[2] = {0.f, 0.f}, av[2] = {0.f, 0.f};
+        if (m < a.m) {
+          const size_t at = (size_t)(col0 + n) * a.ldo + m;
+          float g[2], p[2];
+          unpack2<T>(*reinterpret_cast<const uint32_t *>(reinterpret_cast<const T *>(a.gate_in) + at), g[0], g[1]);
+          unpack2<T>(*reinterpret_cast<const uint32_t *>(reinterpret_cast<const T *>(a.up_in) + at), p[0], p[1]);
+          dglu<2>(a.act, v, g, p, dg, dp, av);
+        }
+        put_row2<T>(a, a.gate_out, m, col0 + n, dg);
+        put_row2<T>(a, a.up_out, m, col0 + n, dp);
+        put_row2<T>(a, a.out[0], m, col0 + n, av);
+      } else {
+        // 16-bit results only: parameter gradients, which may be fp32 or accumulated, take the pair kernel
+        put_row2<T>(a, a.out[0], m, col0 + n, v);
       }
     }
   }

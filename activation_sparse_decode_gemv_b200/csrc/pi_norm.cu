@@ -232,7 +232,11 @@ pi_status pi_block_norm_backward(const pi_block_norm_desc *desc, const float *x_
     j.part_post = a.part_post, j.part_pre = a.part_pre, j.part_gate = a.part_gate;
     j.dw_post = dw_post, j.dw_pre = dw_pre, j.dgate = dgate;
     j.G = G, j.tokens = tokens, j.d = d, j.tokens_per_gate = desc->tokens_per_gate, j.accumulate = acc;
-    const dim3 g(cdiv(d, 32), dgate ? 2 + NM::kGateJobs : 2);
+    if (dgate) {
+      const int rows = cdiv(tokens, desc->tokens_per_gate);  // gate rows, at least one of which may be shared
+      j.gate_jobs = rows < NM::kGateJobs ? rows : NM::kGateJobs;
+    }
+    const dim3 g(cdiv(d, 32), 2 + j.gate_jobs);
     PI_CUDA(launch1(NM::norm_join_kernel, g, 256, 0, 0, nullptr, st, j));
   }
   return PI_OK;
@@ -254,13 +258,13 @@ pi_status pi_quantize_i8(const void *x, int x_dtype, int rows, int k, int8_t *q,
   ch = ch <= 1 ? 1 : ch <= 2 ? 2 : 4;
   int threads = cdiv(cdiv(chunks, ch), 32) * 32;
   if (threads > 1024) threads = 1024;
-  const int per_sm = 2048 / threads > 32 ? 32 : 2048 / threads;
-  const dim3 g(rows < sms * per_sm ? rows : sms * per_sm);
-  NM::QuantArgs a{x, q, scales, x_dtype, rows, k};
+  const NM::QuantArgs a{x, q, scales, rows, k};
   cudaStream_t st = (cudaStream_t)stream;
-  PI_CUDA(ch == 1   ? launch1(NM::quantize_i8_kernel<1>, g, threads, 0, 0, nullptr, st, a)
-         : ch == 2 ? launch1(NM::quantize_i8_kernel<2>, g, threads, 0, 0, nullptr, st, a)
-                   : launch1(NM::quantize_i8_kernel<4>, g, threads, 0, 0, nullptr, st, a));
+  static void (*const kern[3][3])(NM::QuantArgs) = {
+      {NM::quantize_i8_kernel<0, 1>, NM::quantize_i8_kernel<0, 2>, NM::quantize_i8_kernel<0, 4>},
+      {NM::quantize_i8_kernel<1, 1>, NM::quantize_i8_kernel<1, 2>, NM::quantize_i8_kernel<1, 4>},
+      {NM::quantize_i8_kernel<2, 1>, NM::quantize_i8_kernel<2, 2>, NM::quantize_i8_kernel<2, 4>}};
+  PI_CUDA(launch1(kern[x_dtype][ch >> 1], dim3(rows < 65535 ? rows : 65535), threads, 0, 0, nullptr, st, a));
   return PI_OK;
 }
 

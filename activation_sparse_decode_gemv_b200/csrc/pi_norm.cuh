@@ -571,25 +571,29 @@ __global__ void __launch_bounds__(1024) norm_bwd_wide_kernel(const BwdArgs a) {
 // Joins the blocks' column sums in block order, 32 columns a block.
 // blockIdx.y: 0 dw_post, 1 dw_pre, 2.. the gate rows that cross from one
 // block's rows into the next's.  Such a row is taken by the first boundary
-// inside it; boundaries are dealt round robin over kGateJobs blocks.
-constexpr int kGateJobs = 16;
+// inside it; boundaries are dealt round robin over the gate's blocks.
+constexpr int kGateJobs = 16;  // at most
 constexpr int kMaxBwdBlocks = 2048;
 struct JoinArgs {
   const float *part_post, *part_pre, *part_gate;
   float *dw_post, *dw_pre, *dgate;
   int G, tokens, d, tokens_per_gate, accumulate;
+  int gate_jobs;  // blocks along y that share the gate rows
 };
 __global__ void __launch_bounds__(256) norm_join_kernel(const JoinArgs a) {
   pdl_wait();
   pdl_launch_dependents();
   __shared__ float buf[8][32];
-  __shared__ int first[kMaxBwdBlocks + 1];  // the blocks' first tokens
+  __shared__ int shared_row[kMaxBwdBlocks];  // by boundary: the gate row that it takes, or -1
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int i = blockIdx.x * 32 + lane;
   const bool in = i < a.d;
   const int job = blockIdx.y;
   if (job >= 2) {
-    for (int c = threadIdx.x; c <= a.G; c += 256) first[c] = first_token(a.tokens, a.G, c);
+    for (int b = threadIdx.x; b < a.G - 1; b += 256) {
+      const int cut = first_token(a.tokens, a.G, b + 1), row = cut / a.tokens_per_gate, g0 = row * a.tokens_per_gate;
+      shared_row[b] = g0 == cut || first_token(a.tokens, a.G, b) > g0 ? -1 : row;
+    }
     __syncthreads();
   }
   auto put = [&](float *out, float s) { *out = a.accumulate ? *out + s : s; };
@@ -611,34 +615,38 @@ __global__ void __launch_bounds__(256) norm_join_kernel(const JoinArgs a) {
     }
     return;
   }
-  // the shared gate row at boundary b (between blocks b and b + 1): its blocks c0..c1-1, false if another boundary has it
-  int group, c1, slot_b;
-  auto shared_row = [&](int b) {
-    const int cut = first[b + 1];
-    group = cut / a.tokens_per_gate;
-    const int g0 = group * a.tokens_per_gate;
-    if (g0 == cut || first[b] > g0) return false;
-    const long long g1 = min((long long)a.tokens, (long long)g0 + a.tokens_per_gate);
-    c1 = min(a.G, (int)((g1 * a.G + a.tokens - 1) / a.tokens));  // blocks whose first token is below g1
-    slot_b = first[b] < g0 ? 1 : 0;
-    return true;
+  // the blocks that share the gate row of boundary b (between blocks b and b + 1) are b .. end_of - 1
+  auto end_of = [&](int row) {
+    const long long g1 = min((long long)a.tokens, ((long long)row + 1) * a.tokens_per_gate);
+    return min(a.G, (int)((g1 * a.G + a.tokens - 1) / a.tokens));  // blocks whose first token is below g1
   };
   // a block's first gate row is in its slot 0, another in slot 1: only the first block can have begun before the row
-  auto part_of = [&](int c, int b) { return a.part_gate[((size_t)c * 2 + (c == b ? slot_b : 0)) * a.d + i]; };
+  auto part_of = [&](int c, int b, int row) {
+    const int slot = c == b && first_token(a.tokens, a.G, b) < row * a.tokens_per_gate;
+    return a.part_gate[((size_t)c * 2 + slot) * a.d + i];
+  };
   // rows shared by up to 8 blocks: a warp each
-  for (int b = (job - 2) + kGateJobs * w; b < a.G - 1; b += kGateJobs * 8) {
-    if (!shared_row(b) || c1 - b > 8 || !in) continue;
-    float s = part_of(b, b);
-    for (int c = b + 1; c < c1; ++c) s += part_of(c, b);
-    put(a.dgate + (size_t)group * a.d + i, s);
+  for (int b = (job - 2) + a.gate_jobs * w; b < a.G - 1; b += a.gate_jobs * 8) {
+    const int row = shared_row[b];
+    if (row < 0) continue;
+    const int end = end_of(row);
+    if (end - b > 8 || !in) continue;
+    float s = part_of(b, b, row);
+    for (int c = b + 1; c < end; ++c) s += part_of(c, b, row);
+    put(a.dgate + (size_t)row * a.d + i, s);
   }
   // longer ones: all warps
-  for (int b = job - 2; b < a.G - 1; b += kGateJobs) {
-    if (!shared_row(b) || c1 - b <= 8) continue;
+  for (int b = job - 2; b < a.G - 1; b += a.gate_jobs) {
+    const int row = shared_row[b];
+    if (row < 0) continue;
+    const int end = end_of(row);
+    if (end - b <= 8) continue;
     float s = 0.f;
     if (in) {
-#pragma unroll 4
-      for (int c = b + w; c < c1; c += 8) s += part_of(c, b);
+      for (int c = b + w; c < end; c += 8) {
+        if (c == b) s += part_of(c, b, row);
+        else s += a.part_gate[(size_t)c * 2 * a.d + i];
+      }
     }
     __syncthreads();
     buf[w][lane] = s;
@@ -646,7 +654,7 @@ __global__ void __launch_bounds__(256) norm_join_kernel(const JoinArgs a) {
     if (w == 0 && in) {
 #pragma unroll
       for (int k = 1; k < 8; ++k) s += buf[k][lane];
-      put(a.dgate + (size_t)group * a.d + i, s);
+      put(a.dgate + (size_t)row * a.d + i, s);
     }
   }
 }
@@ -655,36 +663,89 @@ __global__ void __launch_bounds__(256) norm_join_kernel(const JoinArgs a) {
 // Row r: scale = amax / 127, q = rint(x / scale) (fp32 quotient, ties to
 // even).  A row of zeros has scale 0 and codes 0; a row that holds an
 // infinity or a NaN has scale NaN and codes 0, so its products are NaN.
-PI_DEV void ld8(const void *p, size_t i, int type, float (&v)[8]) {
-  float4 a, b;
-  if (type == T_F32) {
-    a = ld4(p, i, type), b = ld4(p, i + 4, type);
-  } else {
-    const uint4 w = *reinterpret_cast<const uint4 *>(reinterpret_cast<const uint16_t *>(p) + i);
-    const uint2 h[2] = {make_uint2(w.x, w.y), make_uint2(w.z, w.w)};
-    a = ld4(h, 0, type), b = ld4(h, 4, type);
-  }
-  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-}
 struct QuantArgs {
   const void *x;
   int8_t *q;
   float *scales;
-  int type, rows, k;
+  int rows, k;
 };
-PI_DEV uint32_t code4(const float *v, float scale) {
-  uint32_t w = 0;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int q = (int)fminf(127.f, fmaxf(-127.f, rintf(__fdiv_rn(v[j], scale))));
-    w |= (uint32_t)(q & 255) << (8 * j);
+// 8 elements as loaded: 16-bit types stay packed
+template <int TYPE>
+struct Eight {
+  uint4 w[TYPE == T_F32 ? 2 : 1];
+  PI_DEV void load(const void *p, size_t i) {
+    const char *b = static_cast<const char *>(p) + i * (TYPE == T_F32 ? 4 : 2);
+    w[0] = *reinterpret_cast<const uint4 *>(b);
+    if constexpr (TYPE == T_F32) w[1] = *reinterpret_cast<const uint4 *>(b + 16);
   }
-  return w;
+  PI_DEV void clear() {
+#pragma unroll
+    for (auto &x : w) x = make_uint4(0u, 0u, 0u, 0u);
+  }
+  // the larger of m and the largest bits of |x|: they order like the values,
+  // and a NaN above all.  16-bit types: two halves of a word side by side.
+  PI_DEV unsigned amax(unsigned m) const {
+#pragma unroll
+    for (const auto &x : w) {
+      const unsigned v[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) m = TYPE == T_F32 ? max(m, v[j] & 0x7fffffffu) : __vmaxu2(m, v[j] & 0x7fff7fffu);
+    }
+    return m;
+  }
+  PI_DEV void values(float (&v)[8]) const {
+    if constexpr (TYPE == T_F32) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        v[4 * h] = __uint_as_float(w[h].x), v[4 * h + 1] = __uint_as_float(w[h].y);
+        v[4 * h + 2] = __uint_as_float(w[h].z), v[4 * h + 3] = __uint_as_float(w[h].w);
+      }
+    } else {
+      const uint2 h[2] = {make_uint2(w[0].x, w[0].y), make_uint2(w[0].z, w[0].w)};
+      const float4 a = ld4(h, 0, TYPE), b = ld4(h, 4, TYPE);
+      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    }
+  }
+};
+// the value whose |.| has these bits (one half of a packed word for 16-bit types)
+template <int TYPE>
+PI_DEV unsigned f32_bits(unsigned bits) {
+  if constexpr (TYPE == T_F32) return bits;
+  else if constexpr (TYPE == T_BF16) return bits << 16;
+  else return __float_as_uint(__half2float(__ushort_as_half((unsigned short)bits)));
 }
+PI_DEV uint32_t low_bytes(const float *v) {
+  const uint32_t a = __byte_perm(__float_as_uint(v[0]), __float_as_uint(v[1]), 0x0040);
+  const uint32_t b = __byte_perm(__float_as_uint(v[2]), __float_as_uint(v[3]), 0x0040);
+  return __byte_perm(a, b, 0x5410);
+}
+// Codes of 8 elements.  By definition a code is the nearest integer to the
+// fp32 quotient, ties to even.  x inv (inv = 1 / scale) is within 3e-5 of that
+// quotient (127 x 2^-22), so where it is further than 1e-4 from a tie it
+// rounds alike; adding 1.5 * 2^23 rounds it and leaves the code in the low byte.
+// Elements nearer to a tie, and rows whose scale is too small for its inverse,
+// divide.
+PI_DEV uint2 codes8(const float (&v)[8], float scale, float inv) {
+  constexpr float kRound = 12582912.f;
+  float t[8], off = 0.f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float x = v[j] * inv;
+    t[j] = x + kRound;
+    off = fmaxf(off, fabsf(x - (t[j] - kRound)));
+  }
+  if (off > 0.4999f || inv == 0.f) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      t[j] = fminf(127.f, fmaxf(-127.f, rintf(__fdiv_rn(v[j], scale)))) + kRound;
+  }
+  return make_uint2(low_bytes(t), low_bytes(t + 4));
+}
+
 // One block per row; CH chunks of 8 elements a thread, all loads in flight
 // together and kept as loaded until they are coded.  Rows longer than CH
 // chunks a block (k > 32768) are read again from L2.
-template <int CH>
+template <int TYPE, int CH>
 __global__ void __launch_bounds__(1024) quantize_i8_kernel(const QuantArgs a) {
   __shared__ unsigned buf[2][32];
   pdl_wait();
@@ -693,47 +754,47 @@ __global__ void __launch_bounds__(1024) quantize_i8_kernel(const QuantArgs a) {
   const int step = blockDim.x * 8;
   for (int r = blockIdx.x, it = 0; r < a.rows; r += gridDim.x, ++it) {
     const size_t row = (size_t)r * a.k;
-    unsigned amax = 0;  // bits of |x|: they order like the values, and a NaN above all
-    float v[CH][8];
+    Eight<TYPE> e[CH];
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       const int i = threadIdx.x * 8 + c * step;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[c][j] = 0.f;
-      if (i < a.k) ld8(a.x, row + i, a.type, v[c]);
+      if (i < a.k) e[c].load(a.x, row + i);
+      else e[c].clear();
     }
+    unsigned m = 0;
 #pragma unroll
-    for (int c = 0; c < CH; ++c)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) amax = max(amax, __float_as_uint(v[c][j]) & 0x7fffffffu);
+    for (int c = 0; c < CH; ++c) m = e[c].amax(m);
     for (int i = threadIdx.x * 8 + CH * step; i < a.k; i += step) {
-      float t[8];
-      ld8(a.x, row + i, a.type, t);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) amax = max(amax, __float_as_uint(t[j]) & 0x7fffffffu);
+      Eight<TYPE> t;
+      t.load(a.x, row + i);
+      m = t.amax(m);
     }
-    amax = __reduce_max_sync(0xffffffffu, amax);
+    if constexpr (TYPE != T_F32) m = max(m & 0xffffu, m >> 16);
+    m = __reduce_max_sync(0xffffffffu, m);
     if (nw > 1) {
-      if (lane == 0) buf[it & 1][warp] = amax;
+      if (lane == 0) buf[it & 1][warp] = m;
       __syncthreads();
-      amax = __reduce_max_sync(0xffffffffu, lane < nw ? buf[it & 1][lane] : 0u);
+      m = __reduce_max_sync(0xffffffffu, lane < nw ? buf[it & 1][lane] : 0u);
     }
+    const unsigned amax = f32_bits<TYPE>(m);
     const bool bad = amax >= 0x7f800000u;
     const float scale = bad ? __uint_as_float(0x7fffffffu) : __fdiv_rn(__uint_as_float(amax), 127.f);
     if (threadIdx.x == 0) a.scales[r] = scale;
     const bool zero = bad || scale == 0.f;
-    auto put = [&](int i, const float (&t)[8]) {
-      *reinterpret_cast<uint2 *>(a.q + row + i) =
-          zero ? make_uint2(0u, 0u) : make_uint2(code4(t, scale), code4(t + 4, scale));
+    const float inv = scale > 1e-30f ? __frcp_rn(scale) : 0.f;
+    auto put = [&](int i, const Eight<TYPE> &t) {
+      float v[8];
+      t.values(v);
+      *reinterpret_cast<uint2 *>(a.q + row + i) = zero ? make_uint2(0u, 0u) : codes8(v, scale, inv);
     };
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       const int i = threadIdx.x * 8 + c * step;
-      if (i < a.k) put(i, v[c]);
+      if (i < a.k) put(i, e[c]);
     }
     for (int i = threadIdx.x * 8 + CH * step; i < a.k; i += step) {
-      float t[8];
-      ld8(a.x, row + i, a.type, t);
+      Eight<TYPE> t;
+      t.load(a.x, row + i);
       put(i, t);
     }
   }
