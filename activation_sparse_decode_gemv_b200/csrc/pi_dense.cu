@@ -15,10 +15,10 @@
 struct pi_gated_ffn {
   pi_gated_ffn_desc d;
   // weight maps (valid when maps_ok): 64-row boxes of each matrix, which serve
-  // as K-major rows of 64 neurons and as MN-major 64 x 64 blocks, and
-  // 128-neuron boxes of the down matrix
+  // as K-major rows of 64 neurons and as MN-major 64 x 64 blocks, and boxes of
+  // 128 neurons
   bool maps_ok;
-  CUtensorMap gate64, up64, down64, down128;
+  CUtensorMap gate64, up64, gate128, up128, down64, down128;
 };
 
 namespace {
@@ -121,12 +121,25 @@ struct Plan {
 // the L2's rate per SM, plus the epilogue that no MMA covers.
 double pair_cost(long long tiles, int pairs, int kb, int mb, int nt) {
   const double mma = 2.0 * mb * nt, load = (mb * 16384 + nt * 64) / 42.0;
-  return (double)((tiles + pairs - 1) / pairs) * (kb * (mma > load ? mma : load) + (mb == 2 ? 3000.0 : 1000.0));
+  return (double)((tiles + pairs - 1) / pairs) * (kb * (mma > load ? mma : load) + (mb * nt > 256 ? 3000.0 : 1000.0));
 }
 
-// m_rows: features of a 128-row tile (64 for the gate | up product).  max_mb,
-// nt192: the tilings built for this product.
-Plan choose(int m, int m_rows, int n, int kb, int sms, int max_mb, bool nt192) {
+// Tilings of the CTA-pair kernel that are built for a product.
+struct Tilings {
+  int n;
+  struct {
+    int mb, nt;
+  } t[4];
+};
+constexpr Tilings kGluTilings{2, {{2, 256}, {2, 128}}};
+constexpr Tilings kDgluTilings{2, {{1, 256}, {1, 128}}};
+constexpr Tilings kStoreTilings{4, {{2, 256}, {2, 192}, {1, 256}, {1, 128}}};
+// one block: the scaling epilogue costs more than the B reads that two save (2011 x 5120 x 13824: 126 us
+// against 135)
+constexpr Tilings kI8Tilings{2, {{1, 256}, {1, 128}}};
+
+// m_rows: features of a 128-row block (64 for the gate | up product).
+Plan choose(int m, int m_rows, int n, int kb, int sms, const Tilings &tilings) {
   Plan p{};
   p.mb = 1;
   if (n <= 128) {
@@ -142,12 +155,11 @@ Plan choose(int m, int m_rows, int n, int kb, int sms, int max_mb, bool nt192) {
     return p;
   }
   double best = 0;
-  for (int mb = 1; mb <= max_mb; ++mb)
-    for (int nt = 128; nt <= 256; nt += 64) {
-      if (nt == 192 ? !nt192 || mb != 2 : nt == 128 && mb == 2) continue;
-      const double c = pair_cost((long long)cdiv(m, 2 * mb * m_rows) * cdiv(n, nt), pairs, kb, mb, nt);
-      if (best == 0 || c < best) best = c, p.mb = mb, p.nt = nt;
-    }
+  for (int i = 0; i < tilings.n; ++i) {
+    const auto &t = tilings.t[i];
+    const double c = pair_cost((long long)cdiv(m, 2 * t.mb * m_rows) * cdiv(n, t.nt), pairs, kb, t.mb, t.nt);
+    if (i == 0 || c < best) best = c, p.mb = t.mb, p.nt = t.nt;
+  }
   return p;
 }
 
@@ -163,14 +175,18 @@ cudaError_t run_plan(GM::Args &a, const Plan &p, int dtype, int m_rows, int sms,
   a.nt = cdiv(a.n, p.nt);
   a.idesc = idesc(dtype, EPI == GM::E_I8, p.split ? 128 : 256, p.nt, AMN, 0);
   if (!p.split) {
-    if constexpr (EPI == GM::E_STORE || EPI == GM::E_GLU) {
-      if (p.mb == 2 && p.nt == 256) return pair_launch<EPI, AMN, 0, 2, 256, T>(a, sms, st);
+    if constexpr (EPI == GM::E_GLU) {
+      return p.nt == 256 ? pair_launch<EPI, AMN, 0, 2, 256, T>(a, sms, st)
+                         : pair_launch<EPI, AMN, 0, 2, 128, T>(a, sms, st);
+    } else {
+      if constexpr (EPI == GM::E_STORE) {
+        if (p.mb == 2)
+          return p.nt == 256 ? pair_launch<EPI, AMN, 0, 2, 256, T>(a, sms, st)
+                             : pair_launch<EPI, AMN, 0, 2, 192, T>(a, sms, st);
+      }
+      return p.nt == 256 ? pair_launch<EPI, AMN, 0, 1, 256, T>(a, sms, st)
+                         : pair_launch<EPI, AMN, 0, 1, 128, T>(a, sms, st);
     }
-    if constexpr (EPI == GM::E_STORE) {
-      if (p.mb == 2) return pair_launch<EPI, AMN, 0, 2, 192, T>(a, sms, st);
-    }
-    return p.nt == 256 ? pair_launch<EPI, AMN, 0, 1, 256, T>(a, sms, st)
-                       : pair_launch<EPI, AMN, 0, 1, 128, T>(a, sms, st);
   }
   switch (p.nt) {
   case 16:
@@ -218,8 +234,8 @@ pi_status ffn_forward(const pi_gated_ffn *h, const void *u, int tokens, void *y,
     GM::Args a{};
     a.m = f, a.n = tokens, a.nprob = 1;
     a.kb = a.kb_seg = cdiv(d, 64);
-    const Plan p = choose(f, 64, tokens, a.kb, sms, 2, false);
-    a.ma[0] = h->gate64, a.ma[1] = h->up64;
+    const Plan p = choose(f, 64, tokens, a.kb, sms, kGluTilings);
+    a.ma[0] = p.split ? h->gate64 : h->gate128, a.ma[1] = p.split ? h->up64 : h->up128;
     if (!map16(&a.mb[0], u, tokens, d, p.b_rows())) return PI_ERR_CUDA;
     a.out[0] = w.a;
     a.ldo = f;
@@ -231,7 +247,7 @@ pi_status ffn_forward(const pi_gated_ffn *h, const void *u, int tokens, void *y,
   GM::Args a{};
   a.m = d, a.n = tokens, a.nprob = 1;
   a.kb = a.kb_seg = cdiv(f, 64);
-  const Plan p = choose(d, 128, tokens, a.kb, sms, 2, true);
+  const Plan p = choose(d, 128, tokens, a.kb, sms, kStoreTilings);
   a.ma[0] = h->down64;
   if (!map16(&a.mb[0], w.a, tokens, f, p.b_rows())) return PI_ERR_CUDA;
   a.out[0] = y;
@@ -255,7 +271,7 @@ pi_status ffn_backward(const pi_gated_ffn *h, const void *u, const void *gate, c
     GM::Args a{};
     a.m = f, a.n = tokens, a.nprob = 1;
     a.kb = a.kb_seg = cdiv(d, 64);
-    const Plan p = choose(f, 128, tokens, a.kb, sms, 1, false);
+    const Plan p = choose(f, 128, tokens, a.kb, sms, kDgluTilings);
     a.ma[0] = h->down128;
     if (!map16(&a.mb[0], dy, tokens, d, p.b_rows())) return PI_ERR_CUDA;
     if (!p.split && (!map_2d(&a.ma[1], gate, true, (uint64_t)f, (uint64_t)tokens, 128, (uint32_t)p.nt, false) ||
@@ -309,7 +325,7 @@ pi_status ffn_backward(const pi_gated_ffn *h, const void *u, const void *gate, c
     a.m = d, a.n = tokens, a.nprob = 1;
     a.kb_seg = cdiv(f, 64);
     a.kb = 2 * a.kb_seg;
-    const Plan p = choose(d, 128, tokens, a.kb, sms, 2, true);
+    const Plan p = choose(d, 128, tokens, a.kb, sms, kStoreTilings);
     a.ma[0] = h->gate64, a.ma[1] = h->up64;
     if (!map16(&a.mb[0], w.dg, tokens, f, p.b_rows()) || !map16(&a.mb[1], w.dp, tokens, f, p.b_rows()))
       return PI_ERR_CUDA;
@@ -343,6 +359,7 @@ pi_status pi_gated_ffn_create(const pi_gated_ffn_desc *desc, pi_gated_ffn_t *out
   h->d = D;
   const int d = D.d_model, f = D.d_ffn;
   h->maps_ok = map16(&h->gate64, D.w_gate, f, d, 64) && map16(&h->up64, D.w_up, f, d, 64) &&
+               map16(&h->gate128, D.w_gate, f, d, 128) && map16(&h->up128, D.w_up, f, d, 128) &&
                map16(&h->down64, D.w_down_t, f, d, 64) && map16(&h->down128, D.w_down_t, f, d, 128);
   *out = h;
   return PI_OK;
@@ -430,9 +447,7 @@ pi_status pi_matmul_i8(const int8_t *xq, const float *x_scales, const int8_t *wq
   GM::Args a{};
   a.m = n, a.n = tokens, a.nprob = 1;
   a.kb = a.kb_seg = cdiv(k, 128);
-  // pair tiles of one block: the scaling epilogue costs more than the B reads that two save (2011 x
-  // 5120 x 13824: 126 against 135 us)
-  const Plan p = choose(n, 128, tokens, a.kb, sms, 1, false);
+  const Plan p = choose(n, 128, tokens, a.kb, sms, kI8Tilings);
   if (!map_2d(&a.ma[0], wq, false, (uint64_t)k, (uint64_t)n, 128, 128, true) ||
       !map_2d(&a.mb[0], xq, false, (uint64_t)k, (uint64_t)tokens, 128, (uint32_t)p.b_rows(), true))
     return PI_ERR_CUDA;

@@ -85,9 +85,12 @@ PI_DEV void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-PI_DEV float2 ld_cluster_f32x2(uint32_t addr) {
-  float2 v;
-  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+PI_DEV float4 ld_cluster_f32x4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
   return v;
 }
 PI_DEV void mbar_arrive_cluster(uint32_t cluster_addr) {
@@ -181,6 +184,29 @@ PI_DEV void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
   asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
 }
 
+// 16 columns of tensor memory into registers, as a load to be waited for: an
+// epilogue starts the next columns' load before it works on the present ones.
+PI_DEV void tmem_ld16_start(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+// the loads started so far are done; r's values may be used after this only
+PI_DEV void tmem_ld16_wait(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
+PI_DEV void as_floats(const uint32_t (&r)[16], float (&v)[16]) {
+#pragma unroll
+  for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(r[j]);
+}
+
 // operand descriptor of K step j (32 bytes of k per row, or 16 k) in a stage
 template <int MN>
 PI_DEV uint64_t operand_desc(uint32_t base, int j) {
@@ -210,11 +236,27 @@ PI_DEV float sigmoid(float g) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.f + t));
   return s;
 }
+// The normal distribution's tail Phi(-|g|) = erfc(x) / 2 at x = |g| / sqrt 2,
+// by Abramowitz and Stegun 7.1.26 (absolute error of erf 1.5e-7); e = e^(-x^2)
+// = e^(-g^2/2) is the density's factor too.  The tail is taken as such, not as
+// 1 - erf, so that it keeps its relative accuracy.
+PI_DEV float normal_tail(float g, float &e) {
+  float t;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * g * -0.72134752f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(fmaf(0.3275911f * 0.70710678f, fabsf(g), 1.f)));
+  float y = fmaf(t, 1.061405429f, -1.453152027f);
+  y = fmaf(t, y, 1.421413741f);
+  y = fmaf(t, y, -0.284496736f);
+  y = fmaf(t, y, 0.254829592f);
+  return 0.5f * t * y * e;
+}
 template <int ACT>
 PI_DEV float gate_phi(float g) {
   if constexpr (ACT == G_SILU) return g * sigmoid(g);
   if constexpr (ACT == G_RELU) return g < 0.f ? 0.f : g;  // NaN stays NaN
-  return 0.5f * g * (1.f + erff(g * 0.70710678f));
+  float e;
+  const float t = normal_tail(g, e);
+  return g * (g > 0.f ? 1.f - t : t);
 }
 template <int ACT>
 PI_DEV void gate_phi_grad(float g, float &phi, float &slope) {
@@ -226,21 +268,20 @@ PI_DEV void gate_phi_grad(float g, float &phi, float &slope) {
     phi = g < 0.f ? 0.f : g;
     slope = g > 0.f ? 1.f : 0.f;
   } else {
-    const float c = 0.5f * (1.f + erff(g * 0.70710678f));
+    float e;
+    const float t = normal_tail(g, e), c = g > 0.f ? 1.f - t : t;
     phi = g * c;
-    slope = c + g * 0.39894228f * __expf(-0.5f * g * g);
+    slope = fmaf(g * 0.39894228f, e, c);
   }
 }
 
 // ---------------------------------------------------------------- element epilogues
 // NC consecutive columns n0.. of feature m (the lane's row); E_I8 sums are
-// int32 bits.  `ok` is m < a.m.  Whole 32-feature, NC-column pieces of 16-bit
-// matrices move as 4-byte words of two features: a lane pair swaps halves, so
-// that the even lane holds both features of an even column and the odd lane
-// those of the next column.  That costs 3 instructions an element where the
-// guarded scalar form costs about 24, which the CTA-pair kernel's single
-// accumulator set (MB = 2) would expose: 68% tensor-pipe activity against 86%
-// (dW of 4096 x 5120 x 5120).
+// int32 bits.  16-bit matrices move as 4-byte words of two features: a lane
+// pair swaps halves, so that the even lane holds both features of an even
+// column and the odd lane those of the next column.  That costs 3 instructions
+// an element where a guarded scalar form costs about 24.  Matrices of an odd
+// row length (the 8-bit product's y only) take the scalar form.
 template <typename T>
 PI_DEV uint32_t pack2(float lo, float hi) {
   if constexpr (sizeof(T) == 2 && __is_same(T, __half)) {
@@ -265,33 +306,37 @@ PI_DEV uint32_t pair_swap(uint32_t w) {
   const uint32_t r = __shfl_xor_sync(0xffffffffu, w, 1);
   return __byte_perm(w, r, (threadIdx.x & 1) ? 0x3276 : 0x5410);
 }
-// the warp's 32 features and NC columns lie inside the matrix, and words of two features are aligned
-template <int NC>
-PI_DEV bool whole_piece(const Args &a, int m, int n0) {
-  return (m | 31) < a.m && n0 + NC <= a.n && (a.ldo & 1) == 0;
-}
-
 template <int NC, typename T>
-PI_DEV void put_t(const Args &a, void *out, int m, int n0, bool ok, const float (&v)[NC]) {
-  static_assert(NC % 2 == 0, "whole words");
-  {
-    if (whole_piece<NC>(a, m, n0)) {
-      char *p = reinterpret_cast<char *>(reinterpret_cast<T *>(out) + (size_t)(n0 + (threadIdx.x & 1)) * a.ldo + (m & ~1));
-      const long long step = 4 * a.ldo;
+PI_DEV void put_t(const Args &a, void *out, int m, int n0, const float (&v)[NC]) {
+  if ((a.ldo & 1) == 0) {  // the number of features is even too
+    const int n = n0 + (threadIdx.x & 1);
+    char *p = reinterpret_cast<char *>(reinterpret_cast<T *>(out) + (size_t)n * a.ldo + (m & ~1));
+    const long long step = 4 * a.ldo;
+    const bool in = m < a.m;
+    if (n0 + NC <= a.n) {
 #pragma unroll
-      for (int j = 0; j < NC; j += 2, p += step) *reinterpret_cast<uint32_t *>(p) = pair_swap(pack2<T>(v[j], v[j + 1]));
-      return;
+      for (int j = 0; j < NC; j += 2, p += step) {
+        const uint32_t w = pair_swap(pack2<T>(v[j], v[j + 1]));
+        if (in) *reinterpret_cast<uint32_t *>(p) = w;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < NC; j += 2, p += step) {
+        const uint32_t w = pair_swap(pack2<T>(v[j], v[j + 1]));
+        if (in && n + j < a.n) *reinterpret_cast<uint32_t *>(p) = w;
+      }
     }
+    return;
   }
-  if (!ok) return;
+  if (m >= a.m) return;
   T *p = reinterpret_cast<T *>(out) + (size_t)n0 * a.ldo + m;
 #pragma unroll
   for (int j = 0; j < NC; ++j)
     if (n0 + j < a.n) p[(size_t)j * a.ldo] = Elem<T>::from(v[j]);
 }
 template <int NC>
-PI_DEV void put_f32(const Args &a, void *out, int m, int n0, bool ok, const float (&v)[NC]) {
-  if (!ok) return;
+PI_DEV void put_f32(const Args &a, void *out, int m, int n0, const float (&v)[NC]) {
+  if (m >= a.m) return;
   float *p = reinterpret_cast<float *>(out) + (size_t)n0 * a.ldo + m;
   if (n0 + NC <= a.n) {
 #pragma unroll
@@ -303,49 +348,49 @@ PI_DEV void put_f32(const Args &a, void *out, int m, int n0, bool ok, const floa
     if (n0 + j < a.n) p[(size_t)j * a.ldo] = v[j];
 }
 template <int NC, typename T>
-PI_DEV void add_t(const Args &a, const void *out, int m, int n0, bool ok, float (&v)[NC]) {
+PI_DEV void add_t(const Args &a, const void *out, int m, int n0, float (&v)[NC]) {
   const T *p = reinterpret_cast<const T *>(out) + (size_t)n0 * a.ldo + m;
 #pragma unroll
   for (int j = 0; j < NC; ++j)
-    if (ok && n0 + j < a.n) {
+    if (m < a.m && n0 + j < a.n) {
       if constexpr (__is_same(T, float)) v[j] += p[(size_t)j * a.ldo];
       else v[j] += Elem<T>::to(p[(size_t)j * a.ldo]);
     }
 }
 // out: fp32 or T; acc: what is there is added first, and the sum is rounded once
 template <int NC, typename T>
-PI_DEV void put_cols(const Args &a, void *out, int m, int n0, bool ok, float (&v)[NC], int type, int acc) {
+PI_DEV void put_cols(const Args &a, void *out, int m, int n0, float (&v)[NC], int type, int acc) {
   if (type == O_F32) {
-    if (acc) add_t<NC, float>(a, out, m, n0, ok, v);
-    put_f32<NC>(a, out, m, n0, ok, v);
+    if (acc) add_t<NC, float>(a, out, m, n0, v);
+    put_f32<NC>(a, out, m, n0, v);
   } else {
-    if (acc) add_t<NC, T>(a, out, m, n0, ok, v);
-    put_t<NC, T>(a, out, m, n0, ok, v);
+    if (acc) add_t<NC, T>(a, out, m, n0, v);
+    put_t<NC, T>(a, out, m, n0, v);
   }
 }
 
-// features m, m + 1 (m even) of token n
+// features m .. m + 3 (m a multiple of 4) of token n
 template <typename T>
-PI_DEV void put_row2(const Args &a, void *out, int m, int n, const float (&v)[2]) {
+PI_DEV void put_row4(const Args &a, void *out, int m, int n, const float (&v)[4]) {
   if (m >= a.m) return;
   T *p = reinterpret_cast<T *>(out) + (size_t)n * a.ldo + m;
-  if constexpr (__is_same(T, float)) {
-    p[0] = v[0];
-    if (m + 1 < a.m) p[1] = v[1];
-  } else {
-    if ((a.ldo & 1) == 0) {  // a.m is even too: ldo is the row length
-      *reinterpret_cast<uint32_t *>(p) = pack2<T>(v[0], v[1]);
-    } else {
-      p[0] = Elem<T>::from(v[0]);
-      if (m + 1 < a.m) p[1] = Elem<T>::from(v[1]);
-    }
+  if ((a.ldo & 3) == 0) {  // the number of features is a multiple of 4 too
+    if constexpr (__is_same(T, float)) *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
+    else *reinterpret_cast<uint2 *>(p) = make_uint2(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]));
+    return;
   }
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (m + j < a.m) {
+      if constexpr (__is_same(T, float)) p[j] = v[j];
+      else p[j] = Elem<T>::from(v[j]);
+    }
 }
 
 template <int NC>
-PI_DEV void epi_i8(const Args &a, int m, int n0, bool ok, const float (&v)[NC]) {
-  const float sm = ok ? __ldg(a.s_m + m) : 0.f;
-  const float b = ok && a.bias ? __ldg(a.bias + m) : 0.f;
+PI_DEV void epi_i8(const Args &a, int m, int n0, const float (&v)[NC]) {
+  const float sm = m < a.m ? __ldg(a.s_m + m) : 0.f;
+  const float b = m < a.m && a.bias ? __ldg(a.bias + m) : 0.f;
   float o[NC], sn[NC];
   if (NC % 4 == 0 && n0 + NC <= a.n) {
 #pragma unroll
@@ -359,9 +404,9 @@ PI_DEV void epi_i8(const Args &a, int m, int n0, bool ok, const float (&v)[NC]) 
   }
 #pragma unroll
   for (int j = 0; j < NC; ++j) o[j] = fmaf((float)__float_as_int(v[j]) * sn[j], sm, b);
-  if (a.out_type == O_F32) put_f32<NC>(a, a.out[0], m, n0, ok, o);
-  else if (a.out_type == O_F16) put_t<NC, __half>(a, a.out[0], m, n0, ok, o);
-  else put_t<NC, __nv_bfloat16>(a, a.out[0], m, n0, ok, o);
+  if (a.out_type == O_F32) put_f32<NC>(a, a.out[0], m, n0, o);
+  else if (a.out_type == O_F16) put_t<NC, __half>(a, a.out[0], m, n0, o);
+  else put_t<NC, __nv_bfloat16>(a, a.out[0], m, n0, o);
 }
 
 template <int NC, int ACT>
@@ -383,45 +428,19 @@ PI_DEV void dglu(int act, const float (&da)[NC], const float (&g)[NC], const flo
   else if (act == G_RELU) dglu_act<NC, G_RELU>(da, g, p, dg, dp, av);
   else dglu_act<NC, G_GELU>(da, g, p, dg, dp, av);
 }
-// NC columns of a 16-bit matrix, as words of two columns of this lane's feature; zero outside
-template <int NC, typename T>
-PI_DEV void load_pairs(const Args &a, const void *in, int m, int n0, bool ok, uint32_t (&w)[(NC + 1) / 2]) {
-  if constexpr (NC % 2 == 0) {
-    if (whole_piece<NC>(a, m, n0)) {
-      const char *p = reinterpret_cast<const char *>(reinterpret_cast<const T *>(in) +
-                                                     (size_t)(n0 + (threadIdx.x & 1)) * a.ldo + (m & ~1));
-      const long long step = 4 * a.ldo;
+// NC columns of a 16-bit matrix of an even row length, as loaded: the lane
+// pair's two features of column n0 + j + (lane & 1); zero outside.  pair_swap
+// makes them two columns of the lane's feature.
+template <int NC>
+PI_DEV void load_words(const Args &a, const void *in, int m, int n0, uint32_t (&w)[NC / 2]) {
+  const int n = n0 + (threadIdx.x & 1);
+  const char *p = reinterpret_cast<const char *>(reinterpret_cast<const uint16_t *>(in) + (size_t)n * a.ldo + (m & ~1));
+  const long long step = 4 * a.ldo;
 #pragma unroll
-      for (int j = 0; j < NC / 2; ++j, p += step) w[j] = *reinterpret_cast<const uint32_t *>(p);
-#pragma unroll
-      for (int j = 0; j < NC / 2; ++j) w[j] = pair_swap(w[j]);
-      return;
-    }
-  }
-  const uint16_t *p = reinterpret_cast<const uint16_t *>(in) + (size_t)n0 * a.ldo + m;
-#pragma unroll
-  for (int j = 0; j < NC; j += 2) {
-    const uint32_t lo = ok && n0 + j < a.n ? p[(size_t)j * a.ldo] : 0u;
-    const uint32_t hi = j + 1 < NC && ok && n0 + j + 1 < a.n ? p[(size_t)(j + 1) * a.ldo] : 0u;
-    w[j / 2] = lo | hi << 16;
-  }
+  for (int j = 0; j < NC; j += 2, p += step)
+    w[j / 2] = m < a.m && n + j < a.n ? *reinterpret_cast<const uint32_t *>(p) : 0u;
 }
-template <int NC, typename T>
-PI_DEV void load_gp(const Args &a, int m, int n0, bool ok, float (&g)[NC], float (&p)[NC]) {
-  uint32_t gw[(NC + 1) / 2], pw[(NC + 1) / 2];
-  load_pairs<NC, T>(a, a.gate_in, m, n0, ok, gw);
-  load_pairs<NC, T>(a, a.up_in, m, n0, ok, pw);
-#pragma unroll
-  for (int j = 0; j < NC; j += 2) {
-    float x, y;
-    unpack2<T>(gw[j / 2], x, y);
-    g[j] = x;
-    if (j + 1 < NC) g[j + 1] = y;
-    unpack2<T>(pw[j / 2], x, y);
-    p[j] = x;
-    if (j + 1 < NC) p[j + 1] = y;
-  }
-}
+
 template <int NC>
 PI_DEV void glu(int act, const float (&g)[NC], const float (&p)[NC], float (&o)[NC]) {
   if (act == G_SILU) {
@@ -462,30 +481,31 @@ PI_DEV void load_a(const Args &a, int map, int blk, int row0, uint32_t dst, Load
 // ================================================================ CTA-pair kernel
 constexpr int kPairThreads = 320;  // producer, MMA issuer, 8 epilogue warps
 constexpr int kPairEpi = 8;
-constexpr int kLead = 2;           // MB = 2: K blocks that one accumulator block runs ahead of the other
+constexpr int kLead = 2;           // one buffer of two blocks: K blocks that block 0 runs ahead of block 1
 
-// A pair's tile is MB blocks of 256 features (128 per CTA) x NT columns.
-// MB = 1: the two accumulator buffers alternate between tiles.  MB = 2: both
-// belong to one tile, which halves the B reads per product.
+// A pair's tile is MB accumulator blocks of 256 rows (128 per CTA) x NT
+// columns: MB x 256 features, or for E_GLU (MB = 2) the gate rows and the up
+// rows of the same 256 neurons, so that a lane holds both of a neuron.  Two
+// blocks halve the B reads per product.  Tensor memory holds BUFS tiles: the
+// accumulators of two tiles alternate where they fit.
 template <int EPI, int MB, int NT>
 struct PairShape {
   static constexpr int NB = NT / 2;            // B rows that one CTA of the pair loads
   static constexpr int ABYTES = MB * 16384;    // MB x 128 rows x 128 bytes
   static constexpr int STAGE = ABYTES + NB * 128;
-  static constexpr int XCH = EPI == E_GLU ? 16384 : 0;  // gate/up exchange, 4 warp pairs x 4 KB
-  static constexpr int FIT = (227 * 1024 - 1536 - XCH) / STAGE;
+  static constexpr int FIT = (227 * 1024 - 1536) / STAGE;
   static constexpr int NS = FIT > 8 ? 8 : FIT;
-  static constexpr int XCH_OFF = NS * STAGE;
-  static constexpr int CTRL_OFF = XCH_OFF + XCH;
+  static constexpr int CTRL_OFF = NS * STAGE;
   static constexpr int SMEM = CTRL_OFF + 512 + 1024;  // + alignment slack
-  static constexpr uint32_t TMEM_COLS = 2 * NT <= 256 ? 256 : 512;
-  static_assert(NS >= 2 * kLead || MB == 1, "ring too shallow");
+  static constexpr int BUFS = 2 * MB * NT <= 512 ? 2 : 1;
+  static constexpr uint32_t TMEM_COLS = BUFS * MB * NT <= 256 ? 256 : 512;
+  static_assert(NS >= 2 * kLead || BUFS == 2, "ring too shallow");
   static_assert(SMEM <= 227 * 1024, "shared memory");
 };
 
 template <int NS>
 struct Ctrl {
-  uint64_t full[NS], empty[NS], accfull[2], accfree[2];
+  uint64_t full[NS], empty[NS], accfull[4], accfree[4];  // acc*: by accumulator block
   uint32_t tmem;
   int abort_flag;
 };
@@ -515,7 +535,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     pair_gemm_kernel(const __grid_constant__ Args a) {
   using S = PairShape<EPI, MB, NT>;
   constexpr bool I8 = EPI == E_I8;
-  constexpr int MROWS = EPI == E_GLU ? 64 : 128;  // features of one CTA's half block
+  constexpr int BLKS = S::BUFS * MB;             // accumulator blocks in tensor memory
+  static_assert(EPI != E_GLU || MB == 2, "gate block and up block");
   extern __shared__ unsigned char smem_raw[];
   // the same offset in both CTAs of the pair (the dynamic shared window starts at the same place)
   unsigned char *smem = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -532,7 +553,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       mbar_init(&C.full[s], 1);   // the leader's expect_tx; both CTAs' copies complete the bytes
       mbar_init(&C.empty[s], 1);  // the leader's commit
     }
-    for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < BLKS; ++b) {
       mbar_init(&C.accfull[b], 1);
       mbar_init(&C.accfree[b], 2 * kPairEpi);  // the epilogue warps of both CTAs
     }
@@ -546,10 +567,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   tc_fence_after();
   const uint32_t tmem = C.tmem;
   volatile int *abort_flag = &C.abort_flag;
-  // accumulator block b of this CTA's tc-th tile: its buffer, and the parity of the buffer's tc-th use
-  auto buf_of = [](int tc, int b) { return MB == 1 ? tc & 1 : b; };
-  auto par_of = [](int tc) { return (unsigned)(MB == 1 ? (tc >> 1) & 1 : tc & 1); };
-  constexpr int FIRST_REUSE = MB == 1 ? 2 : 1;
+  // accumulator block b of this CTA's tc-th tile, and the parity of that block's use
+  auto buf_of = [](int tc, int b) { return S::BUFS == 2 ? (tc & 1) * MB + b : b; };
+  auto par_of = [](int tc) { return (unsigned)(S::BUFS == 2 ? (tc >> 1) & 1 : tc & 1); };
+  // first row of this CTA's half of block b of tile m
+  auto row_of = [&](int m, int b) { return ((EPI == E_GLU ? m : m * MB + b) * 2 + rank) * 128; };
 
   pdl_wait();
   pdl_launch_dependents();
@@ -568,7 +590,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           // that reads them (from HBM those reads left 783 TFLOP/s, from L2 1150)
 #pragma unroll
           for (int b = 0; b < MB; ++b) {
-            const int row0 = ((at.m * MB + b) * 2 + rank) * MROWS;
+            const int row0 = row_of(at.m, b);
             if (row0 >= a.m) continue;
             prefetch_l2_2d(&a.ma[1], row0, at.n * NT);
             prefetch_l2_2d(&a.ma[2], row0, at.n * NT);
@@ -586,8 +608,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           k_at(a, at.prob, kb, map, blk);
           auto load = [&](uint32_t d, const CUtensorMap *tm, int x, int y) { tma_load_2d_pair(d, tm, x, y, bar); };
 #pragma unroll
-          for (int b = 0; b < MB; ++b)
-            load_a<EPI, AMN>(a, map, blk, ((at.m * MB + b) * 2 + rank) * MROWS, dst + b * 16384, load);
+          for (int b = 0; b < MB; ++b) {
+            if constexpr (EPI == E_GLU) load(dst + b * 16384, &a.ma[b], blk * 64, row_of(at.m, b));
+            else load_a<EPI, AMN>(a, map, blk, row_of(at.m, b), dst + b * 16384, load);
+          }
           const CUtensorMap *tb = &a.mb[map];
           if constexpr (BMN) {
 #pragma unroll
@@ -614,7 +638,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       bool ok = true;
       auto wait_full = [&](int st, unsigned p) { return mbar_wait_cluster(&C.full[st], p, abort_flag, a.status); };
       auto wait_free = [&](int b) {
-        const bool r = tc < FIRST_REUSE ||
+        const bool r = tc < S::BUFS ||
                        mbar_wait_cluster(&C.accfree[buf_of(tc, b)], par_of(tc) ^ 1u, abort_flag, a.status);
         tc_fence_after();
         return r;
@@ -628,16 +652,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                      (first && j == 0) ? 0u : 1u);
       };
       for (int t = pair; t < tiles && ok; t += npairs, ++tc) {
-        if (MB == 1) {
-          if (!(ok = wait_free(0))) break;
+        if constexpr (S::BUFS == 2) {
+          for (int b = 0; b < MB && ok; ++b) ok = wait_free(b);
+          if (!ok) break;
           for (int kb = 0; kb < a.kb; ++kb) {
             if (!(ok = wait_full(s, ph))) break;
             tc_fence_after();
-            issue(0, s, kb == 0);
+#pragma unroll
+            for (int b = 0; b < MB; ++b) issue(b, s, kb == 0);
             mma_commit_pair(&C.empty[s]);
             if (++s == S::NS) s = 0, ph ^= 1u;
           }
-          if (ok) mma_commit_pair(&C.accfull[buf_of(tc, 0)]);
+          if (ok)
+#pragma unroll
+            for (int b = 0; b < MB; ++b) mma_commit_pair(&C.accfull[buf_of(tc, b)]);
         } else {
           // Block 0 runs kLead K blocks ahead of block 1 at both ends of the
           // tile: its epilogue starts while block 1's last MMAs run, and
@@ -675,88 +703,101 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   } else {
     // ------------------------------------------------------------ epilogue: lane quarter q, column half h
     const int q = warp & 3, h = (warp - 2) >> 2;
-    const int lrow = q * 32 + lane;  // row of this CTA's half block
     int tc = 0;
     bool go = true;
+    auto wait_acc = [&](int b) {
+      const bool r = __all_sync(0xffffffffu, mbar_wait_cluster(&C.accfull[b], par_of(tc), abort_flag, a.status));
+      tc_fence_after();
+      return r;
+    };
+    auto free_acc = [&](int b) {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(mapa(su32(&C.accfree[b]), 0));
+    };
     for (int t = pair; t < tiles && go; t += npairs, ++tc) {
       const TileAt at = tile_at(a, t);
-#pragma unroll 1
-      for (int blk = 0; blk < MB; ++blk) {
-        const int b = buf_of(tc, blk);
-        bool ok = __all_sync(0xffffffffu, mbar_wait_cluster(&C.accfull[b], par_of(tc), abort_flag, a.status));
-        if constexpr (EPI == E_GLU) {
-          // the exchange below needs all 8 warps: agree on going on
-          uint32_t bad;
-          asm volatile(
-              "{\n .reg .pred p, r;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred r, 1, 256, p;\n"
-              " selp.u32 %0, 1, 0, r;\n}\n"
-              : "=r"(bad)
-              : "r"(ok ? 0u : 1u)
-              : "memory");
-          ok = !bad;
+      const int n0 = at.n * NT + h * (NT / 2);
+      auto tmem_of = [&](int b) { return tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * NT + h * (NT / 2)); };
+      // 16-column chunks of this warp inside the matrix; none where its rows are outside
+      auto chunks_of = [&](int m) {
+        return (m & ~31) < a.m ? min(NT / 32, max(0, (a.n - n0 + 15) / 16)) : 0;
+      };
+      if constexpr (EPI == E_GLU) {
+        const int bg = buf_of(tc, 0), bu = buf_of(tc, 1);
+        if (!(go = wait_acc(bg)) || !(go = wait_acc(bu))) break;
+        const int m = row_of(at.m, 0) + q * 32 + lane, nchunks = chunks_of(m);
+        const uint32_t tg = tmem_of(bg), tu = tmem_of(bu);
+        uint32_t rg[16], ru[16];
+        if (nchunks) {
+          tmem_ld16_start(tg, rg);
+          tmem_ld16_start(tu, ru);
         }
-        if (!ok) {
-          go = false;
-          break;
-        }
-        tc_fence_after();
-        const uint32_t tbase = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * NT + h * (NT / 2));
-        const int n0 = at.n * NT + h * (NT / 2);
-        const int half_row0 = ((at.m * MB + blk) * 2 + rank) * MROWS;
-        if constexpr (EPI == E_GLU) {
-          // lanes 0..63 hold gate rows, lanes 64..127 the up rows of the same
-          // neurons: warps q and q + 2 swap half a chunk through shared memory
-          // and each finishes the other half
-          const int neuron = half_row0 + (q & 1) * 32 + lane;
-          const bool in = neuron < a.m;
-          const bool is_up = q >= 2;
-          float *xb = reinterpret_cast<float *>(smem + S::XCH_OFF) + (h * 2 + (q & 1)) * 1024;
-          void *keep = is_up ? a.up_out : a.gate_out;
 #pragma unroll 1
-          for (int c = 0; c < NT / 32; ++c) {
-            float v[16];
-            tmem_ld16(tbase + c * 16, v);
-            float *buf = xb + (c & 1) * 512;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) buf[(is_up ? 256 : 0) + j * 32 + lane] = is_up ? v[j] : v[8 + j];
-            if (keep) put_t<16, T>(a, keep, neuron, n0 + c * 16, in, v);
-            asm volatile("bar.sync %0, 64;" ::"r"(2 + h * 2 + (q & 1)) : "memory");
-            float mine[8], other[8], o[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              mine[j] = is_up ? v[8 + j] : v[j];
-              other[j] = buf[(is_up ? 0 : 256) + j * 32 + lane];
-            }
-            if (is_up) glu<8>(a.act, other, mine, o);
-            else glu<8>(a.act, mine, other, o);
-            put_t<8, T>(a, a.out[0], neuron, n0 + c * 16 + (is_up ? 8 : 0), in, o);
+        for (int c = 0; c < nchunks; ++c) {
+          const int nc = n0 + c * 16;
+          float g[16], p[16], o[16];
+          tmem_ld16_wait(rg);
+          tmem_ld16_wait(ru);
+          as_floats(rg, g);
+          as_floats(ru, p);
+          if (c + 1 < nchunks) {
+            tmem_ld16_start(tg + (c + 1) * 16, rg);
+            tmem_ld16_start(tu + (c + 1) * 16, ru);
           }
-        } else {
-          const int m = half_row0 + lrow;
-          const bool in = m < a.m;
+          if (a.gate_out) put_t<16, T>(a, a.gate_out, m, nc, g);
+          if (a.up_out) put_t<16, T>(a, a.up_out, m, nc, p);
+          glu<16>(a.act, g, p, o);
+          put_t<16, T>(a, a.out[0], m, nc, o);
+        }
+        free_acc(bg);
+        free_acc(bu);
+      } else {
 #pragma unroll 1
-          for (int c = 0; c < NT / 32; ++c) {
-            float v[16];
+        for (int blk = 0; blk < MB; ++blk) {
+          const int b = buf_of(tc, blk);
+          const int m = row_of(at.m, blk) + q * 32 + lane, nchunks = chunks_of(m);
+          const uint32_t tb = tmem_of(b);
+          uint32_t gw[8], pw[8];
+          if constexpr (EPI == E_DGLU) {
+            if (nchunks) {
+              load_words<16>(a, a.gate_in, m, n0, gw);
+              load_words<16>(a, a.up_in, m, n0, pw);
+            }
+          }
+          if (!(go = wait_acc(b))) break;
+          uint32_t r[16];
+          if (nchunks) tmem_ld16_start(tb, r);
+#pragma unroll 1
+          for (int c = 0; c < nchunks; ++c) {
             const int nc = n0 + c * 16;
+            float v[16];
+            tmem_ld16_wait(r);
+            as_floats(r, v);
+            if (c + 1 < nchunks) tmem_ld16_start(tb + (c + 1) * 16, r);
             if constexpr (EPI == E_DGLU) {
-              float g[16], p[16];
-              load_gp<16, T>(a, m, nc, in, g, p);
-              tmem_ld16(tbase + c * 16, v);
-              float dg[16], dp[16], av[16];
+              float g[16], p[16], dg[16], dp[16], av[16];
+#pragma unroll
+              for (int j = 0; j < 16; j += 2) {
+                unpack2<T>(pair_swap(gw[j / 2]), g[j], g[j + 1]);
+                unpack2<T>(pair_swap(pw[j / 2]), p[j], p[j + 1]);
+              }
+              if (c + 1 < nchunks) {
+                load_words<16>(a, a.gate_in, m, nc + 16, gw);
+                load_words<16>(a, a.up_in, m, nc + 16, pw);
+              }
               dglu<16>(a.act, v, g, p, dg, dp, av);
-              put_t<16, T>(a, a.gate_out, m, nc, in, dg);
-              put_t<16, T>(a, a.up_out, m, nc, in, dp);
-              put_t<16, T>(a, a.out[0], m, nc, in, av);
+              put_t<16, T>(a, a.gate_out, m, nc, dg);
+              put_t<16, T>(a, a.up_out, m, nc, dp);
+              put_t<16, T>(a, a.out[0], m, nc, av);
+            } else if constexpr (EPI == E_I8) {
+              epi_i8<16>(a, m, nc, v);
             } else {
-              tmem_ld16(tbase + c * 16, v);
-              if constexpr (EPI == E_I8) epi_i8<16>(a, m, nc, in, v);
-              else put_cols<16, T>(a, a.out[at.prob], m, nc, in, v, a.out_type, a.accumulate);
+              put_cols<16, T>(a, a.out[at.prob], m, nc, v, a.out_type, a.accumulate);
             }
           }
+          free_acc(b);
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(mapa(su32(&C.accfree[b]), 0));
       }
     }
   }
@@ -891,69 +932,78 @@ __global__ void __launch_bounds__(kSplitThreads, 2) split_gemm_kernel(const __gr
   cluster_sync();  // every CTA's partial tile is in its shared memory
   {
     // ------------------------------------------------------------ join: this CTA's slice of the tile, summed in rank order
-    // (two features of a token at a time)
+    // (four features of a token at a time, two such items in flight a thread)
+    constexpr int Q = MROWS / 4;
     const int nv = min(NT, a.n - col0);
-    const int E = nv * MROWS;
-    const int per = ((E + split * 64 - 1) / (split * 64)) * 64;
+    const int E = nv * Q;
+    const int per = ((E + split * 32 - 1) / (split * 32)) * 32;
     const int e0 = rank * per, e1 = min(E, e0 + per);
     const uint32_t red = su32(smem);
-    for (int e = e0 + 2 * tid; e < e1; e += 2 * kSplitThreads) {
-      const int n = e / MROWS, r = e % MROWS;
-      const uint32_t off = red + (uint32_t)(n * 128 + r) * 4;
-      const int m = row0 + r;
-      float v[2] = {0.f, 0.f}, w[2] = {0.f, 0.f};
-      if constexpr (I8) {
-        int s0 = 0, s1 = 0;
+    auto sum = [&](int e, float (&v)[4], float (&w)[4]) {
+      const uint32_t off = red + (uint32_t)((e / Q) * 128 + (e % Q) * 4) * 4;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = w[j] = 0.f;
 #pragma unroll 4
-        for (int c = 0; c < split; ++c) {
-          const float2 f = ld_cluster_f32x2(mapa(off, c));
-          s0 += __float_as_int(f.x), s1 += __float_as_int(f.y);
-        }
-        v[0] = __int_as_float(s0), v[1] = __int_as_float(s1);
-      } else {
-#pragma unroll 4
-        for (int c = 0; c < split; ++c) {
-          const float2 f = ld_cluster_f32x2(mapa(off, c));
-          v[0] += f.x, v[1] += f.y;
+      for (int c = 0; c < split; ++c) {
+        const float4 f = ld_cluster_f32x4(mapa(off, c));
+        if constexpr (I8) {
+          v[0] = __int_as_float(__float_as_int(v[0]) + __float_as_int(f.x));
+          v[1] = __int_as_float(__float_as_int(v[1]) + __float_as_int(f.y));
+          v[2] = __int_as_float(__float_as_int(v[2]) + __float_as_int(f.z));
+          v[3] = __int_as_float(__float_as_int(v[3]) + __float_as_int(f.w));
+        } else {
+          v[0] += f.x, v[1] += f.y, v[2] += f.z, v[3] += f.w;
           if constexpr (EPI == E_GLU) {
-            const float2 g = ld_cluster_f32x2(mapa(off + 256, c));
-            w[0] += g.x, w[1] += g.y;
+            const float4 g = ld_cluster_f32x4(mapa(off + 256, c));
+            w[0] += g.x, w[1] += g.y, w[2] += g.z, w[3] += g.w;
           }
         }
       }
+    };
+    auto finish = [&](int e, float (&v)[4], float (&w)[4]) {
+      const int n = col0 + e / Q, m = row0 + (e % Q) * 4;
+      if (m >= a.m) return;
       if constexpr (EPI == E_GLU) {
-        float o[2];
-        glu<2>(a.act, v, w, o);
-        if (a.gate_out) put_row2<T>(a, a.gate_out, m, col0 + n, v);
-        if (a.up_out) put_row2<T>(a, a.up_out, m, col0 + n, w);
-        put_row2<T>(a, a.out[0], m, col0 + n, o);
+        float o[4];
+        glu<4>(a.act, v, w, o);
+        if (a.gate_out) put_row4<T>(a, a.gate_out, m, n, v);
+        if (a.up_out) put_row4<T>(a, a.up_out, m, n, w);
+        put_row4<T>(a, a.out[0], m, n, o);
       } else if constexpr (EPI == E_I8) {
-        const float sn = __ldg(a.s_n + col0 + n);
+        const float sn = __ldg(a.s_n + n);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
+        for (int j = 0; j < 4; ++j) {
           const int mj = min(m + j, a.m - 1);
           v[j] = fmaf((float)__float_as_int(v[j]) * sn, __ldg(a.s_m + mj), a.bias ? __ldg(a.bias + mj) : 0.f);
         }
-        if (a.out_type == O_F32) put_row2<float>(a, a.out[0], m, col0 + n, v);
-        else if (a.out_type == O_F16) put_row2<__half>(a, a.out[0], m, col0 + n, v);
-        else put_row2<__nv_bfloat16>(a, a.out[0], m, col0 + n, v);
+        if (a.out_type == O_F32) put_row4<float>(a, a.out[0], m, n, v);
+        else if (a.out_type == O_F16) put_row4<__half>(a, a.out[0], m, n, v);
+        else put_row4<__nv_bfloat16>(a, a.out[0], m, n, v);
       } else if constexpr (EPI == E_DGLU) {
-        // features come in pairs (f is a multiple of 8)
-        float dg[2] = {0.f, 0.f}, dp[2] = {0.f, 0.f}, av[2] = {0.f, 0.f};
-        if (m < a.m) {
-          const size_t at = (size_t)(col0 + n) * a.ldo + m;
-          float g[2], p[2];
-          unpack2<T>(*reinterpret_cast<const uint32_t *>(reinterpret_cast<const T *>(a.gate_in) + at), g[0], g[1]);
-          unpack2<T>(*reinterpret_cast<const uint32_t *>(reinterpret_cast<const T *>(a.up_in) + at), p[0], p[1]);
-          dglu<2>(a.act, v, g, p, dg, dp, av);
-        }
-        put_row2<T>(a, a.gate_out, m, col0 + n, dg);
-        put_row2<T>(a, a.up_out, m, col0 + n, dp);
-        put_row2<T>(a, a.out[0], m, col0 + n, av);
+        const size_t at = (size_t)n * a.ldo + m;  // rows of a multiple of 8 features
+        const uint2 gw = *reinterpret_cast<const uint2 *>(reinterpret_cast<const T *>(a.gate_in) + at);
+        const uint2 pw = *reinterpret_cast<const uint2 *>(reinterpret_cast<const T *>(a.up_in) + at);
+        float g[4], p[4], dg[4], dp[4], av[4];
+        unpack2<T>(gw.x, g[0], g[1]);
+        unpack2<T>(gw.y, g[2], g[3]);
+        unpack2<T>(pw.x, p[0], p[1]);
+        unpack2<T>(pw.y, p[2], p[3]);
+        dglu<4>(a.act, v, g, p, dg, dp, av);
+        put_row4<T>(a, a.gate_out, m, n, dg);
+        put_row4<T>(a, a.up_out, m, n, dp);
+        put_row4<T>(a, a.out[0], m, n, av);
       } else {
         // 16-bit results only: parameter gradients, which may be fp32 or accumulated, take the pair kernel
-        put_row2<T>(a, a.out[0], m, col0 + n, v);
+        put_row4<T>(a, a.out[0], m, n, v);
       }
+    };
+    for (int e = e0 + tid; e < e1; e += 2 * kSplitThreads) {
+      float v0[4], w0[4], v1[4], w1[4];
+      const bool two = e + kSplitThreads < e1;
+      sum(e, v0, w0);
+      if (two) sum(e + kSplitThreads, v1, w1);
+      finish(e, v0, w0);
+      if (two) finish(e + kSplitThreads, v1, w1);
     }
   }
   tc_fence_before();

@@ -233,8 +233,9 @@ pi_status pi_block_norm_backward(const pi_block_norm_desc *desc, const float *x_
     j.dw_post = dw_post, j.dw_pre = dw_pre, j.dgate = dgate;
     j.G = G, j.tokens = tokens, j.d = d, j.tokens_per_gate = desc->tokens_per_gate, j.accumulate = acc;
     if (dgate) {
-      const int rows = cdiv(tokens, desc->tokens_per_gate);  // gate rows, at least one of which may be shared
-      j.gate_jobs = rows < NM::kGateJobs ? rows : NM::kGateJobs;
+      const int rows = cdiv(tokens, desc->tokens_per_gate);
+      j.long_rows = (long long)desc->tokens_per_gate * G > 8ll * tokens;  // fewer than G / 8 rows
+      j.gate_jobs = j.long_rows ? rows : rows < NM::kGateJobs ? rows : NM::kGateJobs;
     }
     const dim3 g(cdiv(d, 32), 2 + j.gate_jobs);
     PI_CUDA(launch1(NM::norm_join_kernel, g, 256, 0, 0, nullptr, st, j));

@@ -568,43 +568,56 @@ __global__ void __launch_bounds__(1024) norm_bwd_wide_kernel(const BwdArgs a) {
       *reinterpret_cast<float4 *>(a.part_pre + (size_t)blockIdx.x * a.d + i) = ld4(s_pre + i);
 }
 
-// Joins the blocks' column sums in block order, 32 columns a block.
-// blockIdx.y: 0 dw_post, 1 dw_pre, 2.. the gate rows that cross from one
-// block's rows into the next's.  Such a row is taken by the first boundary
-// inside it; boundaries are dealt round robin over the gate's blocks.
-constexpr int kGateJobs = 16;  // at most
+// Joins the blocks' column sums in block order, 32 columns a block, in jobs
+// along y: dw_post, dw_pre, and the gate rows that cross from one block's rows
+// into the next's.  A gate row shared by many blocks (tokens_per_gate over 8
+// blocks' rows) has a job of its own, summed by all warps; short ones, at most
+// one per boundary between blocks, are dealt to the warps of kGateJobs jobs.
+constexpr int kGateJobs = 16;
 constexpr int kMaxBwdBlocks = 2048;
 struct JoinArgs {
   const float *part_post, *part_pre, *part_gate;
   float *dw_post, *dw_pre, *dgate;
   int G, tokens, d, tokens_per_gate, accumulate;
-  int gate_jobs;  // blocks along y that share the gate rows
+  int long_rows;  // gate rows are long: job 2 + row has row
+  int gate_jobs;
 };
 __global__ void __launch_bounds__(256) norm_join_kernel(const JoinArgs a) {
   pdl_wait();
   pdl_launch_dependents();
   __shared__ float buf[8][32];
-  __shared__ int shared_row[kMaxBwdBlocks];  // by boundary: the gate row that it takes, or -1
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int i = blockIdx.x * 32 + lane;
   const bool in = i < a.d;
   const int job = blockIdx.y;
-  if (job >= 2) {
-    for (int b = threadIdx.x; b < a.G - 1; b += 256) {
-      const int cut = first_token(a.tokens, a.G, b + 1), row = cut / a.tokens_per_gate, g0 = row * a.tokens_per_gate;
-      shared_row[b] = g0 == cut || first_token(a.tokens, a.G, b) > g0 ? -1 : row;
-    }
-    __syncthreads();
-  }
   auto put = [&](float *out, float s) { *out = a.accumulate ? *out + s : s; };
-  if (job < 2) {
-    float *out = job == 0 ? a.dw_post : a.dw_pre;
-    const float *part = job == 0 ? a.part_post : a.part_pre;
-    if (!out) return;
+  // blocks that hold tokens of gate row `row`: [b0, b1)
+  auto blocks_of = [&](int row, int &b0, int &b1) {
+    const long long g0 = (long long)row * a.tokens_per_gate, g1 = min((long long)a.tokens, g0 + a.tokens_per_gate);
+    b1 = min(a.G, (int)((g1 * a.G + a.tokens - 1) / a.tokens));                       // blocks that begin before g1
+    b0 = max(0, min(a.G, (int)(((g0 + 1) * a.G + a.tokens - 1) / a.tokens)) - 1);     // the last that begins by g0
+  };
+  // a block's first gate row is in its slot 0, another in slot 1: only the
+  // first block of a row can have begun before the row
+  auto row_part = [&](int c, int b0, int row) {
+    const int slot = c == b0 && first_token(a.tokens, a.G, b0) < (long long)row * a.tokens_per_gate;
+    return a.part_gate + ((size_t)c * 2 + slot) * a.d;
+  };
+  if (job < 2 || a.long_rows) {
+    float *out = job == 0 ? a.dw_post : job == 1 ? a.dw_pre : a.dgate + (size_t)(job - 2) * a.d;
+    const float *part = job == 0 ? a.part_post : job == 1 ? a.part_pre : a.part_gate;
+    if (job < 2 && !out) return;
+    int b0 = 0, b1 = a.G, stride = 1;
+    if (job >= 2) {
+      blocks_of(job - 2, b0, b1);
+      if (b1 - b0 < 2) return;  // one block's alone: it is stored already
+      stride = 2;
+    }
     float s = 0.f;
     if (in) {
 #pragma unroll 8
-      for (int c = w; c < a.G; c += 8) s += part[(size_t)c * a.d + i];
+      for (int c = b0 + w; c < b1; c += 8)
+        s += (c == b0 && job >= 2 ? row_part(c, b0, job - 2) : part + (size_t)c * stride * a.d)[i];
     }
     buf[w][lane] = s;
     __syncthreads();
@@ -615,47 +628,16 @@ __global__ void __launch_bounds__(256) norm_join_kernel(const JoinArgs a) {
     }
     return;
   }
-  // the blocks that share the gate row of boundary b (between blocks b and b + 1) are b .. end_of - 1
-  auto end_of = [&](int row) {
-    const long long g1 = min((long long)a.tokens, ((long long)row + 1) * a.tokens_per_gate);
-    return min(a.G, (int)((g1 * a.G + a.tokens - 1) / a.tokens));  // blocks whose first token is below g1
-  };
-  // a block's first gate row is in its slot 0, another in slot 1: only the first block can have begun before the row
-  auto part_of = [&](int c, int b, int row) {
-    const int slot = c == b && first_token(a.tokens, a.G, b) < row * a.tokens_per_gate;
-    return a.part_gate[((size_t)c * 2 + slot) * a.d + i];
-  };
-  // rows shared by up to 8 blocks: a warp each
+  // the row at boundary b (between blocks b and b + 1), if the boundary is the first inside it
   for (int b = (job - 2) + a.gate_jobs * w; b < a.G - 1; b += a.gate_jobs * 8) {
-    const int row = shared_row[b];
-    if (row < 0) continue;
-    const int end = end_of(row);
-    if (end - b > 8 || !in) continue;
-    float s = part_of(b, b, row);
-    for (int c = b + 1; c < end; ++c) s += part_of(c, b, row);
-    put(a.dgate + (size_t)row * a.d + i, s);
-  }
-  // longer ones: all warps
-  for (int b = job - 2; b < a.G - 1; b += a.gate_jobs) {
-    const int row = shared_row[b];
-    if (row < 0) continue;
-    const int end = end_of(row);
-    if (end - b <= 8) continue;
+    const int cut = first_token(a.tokens, a.G, b + 1), row = cut / a.tokens_per_gate;
+    if (row * a.tokens_per_gate == cut) continue;
+    int b0, b1;
+    blocks_of(row, b0, b1);
+    if (b0 != b || !in) continue;
     float s = 0.f;
-    if (in) {
-      for (int c = b + w; c < end; c += 8) {
-        if (c == b) s += part_of(c, b, row);
-        else s += a.part_gate[(size_t)c * 2 * a.d + i];
-      }
-    }
-    __syncthreads();
-    buf[w][lane] = s;
-    __syncthreads();
-    if (w == 0 && in) {
-#pragma unroll
-      for (int k = 1; k < 8; ++k) s += buf[k][lane];
-      put(a.dgate + (size_t)row * a.d + i, s);
-    }
+    for (int c = b0; c < b1; ++c) s += row_part(c, b0, row)[i];
+    put(a.dgate + (size_t)row * a.d + i, s);
   }
 }
 
