@@ -6,6 +6,7 @@
 
 #include <atomic>
 #include <cstdint>
+#include <mutex>
 #include <new>
 
 #include "pi_ffn.h"
@@ -50,117 +51,141 @@ cudaError_t pair_launch(const GM::Args &a, int sms, cudaStream_t st) {
 // allocates tensor memory the occupancy calculator answers with one CTA per
 // SM, whatever it allocates, but the hardware runs two.
 __global__ void __launch_bounds__(GM::kSplitThreads) shape_kernel() {}
-template <int NT>
-int resident_clusters(int split) {
-  static DeviceOnce once;
-  static std::atomic<int> cache[64][kMaxSplit + 1];
+struct ClusterCaps {
+  int n[kMaxSplit + 1];  // by split; 0: does not run
+};
+const ClusterCaps *cluster_caps() {
+  static std::mutex mu;
+  static std::atomic<const ClusterCaps *> ready[64];
+  static ClusterCaps caps[64];
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
-  int n = cache[dev][split].load(std::memory_order_relaxed);
-  if (n == 0) {
-    if (once.ensure([] {
-          const cudaError_t e =
-              cudaFuncSetAttribute(shape_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
-          return e != cudaSuccess ? e
-                                  : cudaFuncSetAttribute(shape_kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
-                                                         cudaSharedmemCarveoutMaxShared);
-        }) != cudaSuccess)
-      return 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return nullptr;
+  if (const ClusterCaps *c = ready[dev].load(std::memory_order_acquire)) return c;
+  std::lock_guard<std::mutex> lock(mu);
+  if (cudaFuncSetAttribute(shape_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024) != cudaSuccess ||
+      cudaFuncSetAttribute(shape_kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                           cudaSharedmemCarveoutMaxShared) != cudaSuccess)
+    return nullptr;
+  for (int split = 1; split <= kMaxSplit; ++split) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(split);
     cfg.blockDim = dim3(GM::kSplitThreads);
-    cfg.dynamicSmemBytes = GM::SplitShape<NT>::SMEM;
+    cfg.dynamicSmemBytes = GM::SplitShape<16>::SMEM;  // the largest
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = (unsigned)split;
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
+    int n = 0;
     if (cudaOccupancyMaxActiveClusters(&n, shape_kernel, &cfg) != cudaSuccess) {
       cudaGetLastError();
-      return 0;
+      n = 0;
     }
-    cache[dev][split].store(n, std::memory_order_relaxed);
+    caps[dev].n[split] = n;
   }
-  return n;
+  ready[dev].store(&caps[dev], std::memory_order_release);
+  return &caps[dev];
 }
-// The largest split whose clusters all run at once, at least 4 K blocks each:
-// a second round of clusters would double the time (one token, 5120 x 13824:
-// down product split by 6 70.5 us for the block, by 7 (more clusters than fit)
-// 83.8, by 4 74.3, by 2 97.9).
 template <int EPI, int AMN, int NT, typename T>
-cudaError_t split_launch(const GM::Args &a, cudaStream_t st) {
+cudaError_t split_launch(const GM::Args &a, int split, cudaStream_t st) {
   static DeviceOnce once;
+  using Sh = GM::SplitShape<NT>;
   const auto kern = GM::split_gemm_kernel<EPI, AMN, NT, T>;
   cudaError_t e = once.ensure([&] {
-    // an SM's memory as shared memory: two CTAs are resident
-    cudaError_t r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, GM::SplitShape<NT>::SMEM);
+    const cudaError_t r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::SMEM);
     return r != cudaSuccess ? r
                             : cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout,
                                                    cudaSharedmemCarveoutMaxShared);
   });
   if (e != cudaSuccess) return e;
-  const int tiles = a.mt * a.nt;
-  int split = a.kb / 4 < kMaxSplit ? a.kb / 4 : kMaxSplit;
-  while (split > 1 && resident_clusters<NT>(split) < tiles) --split;
-  if (split < 1) split = 1;
-  return launch1(kern, dim3((unsigned)(tiles * split)), GM::kSplitThreads,
-                 GM::SplitShape<NT>::SMEM, split, nullptr, st, a);
+  return launch1(kern, dim3((unsigned)(a.mt * a.nt * split)), GM::kSplitThreads, Sh::SMEM, split, nullptr, st, a);
 }
 
-// How a product runs.  nt: token columns of a tile; mb: 256-feature blocks of
-// a CTA-pair tile; split: the split-K kernel instead.
+// How a product runs.  nt: token columns of a tile; mb: 256-row blocks of a
+// CTA-pair tile; split: 0 = CTA-pair kernel, else the split-K kernel with
+// clusters of that many CTAs; deep: its one-CTA-per-SM form.  nt = 0: none (the
+// device could not be asked).
 struct Plan {
-  int nt, mb;
-  bool split;
+  int nt, mb, split;
+  bool deep;
   int b_rows() const { return split ? nt : nt / 2; }  // rows of the B box
 };
 
-// Time of a CTA-pair tiling, in SM cycles: rounds of tiles x K blocks x the
-// slower of the MMAs (2 cycles a column and block) and the stage's bytes at
-// the L2's rate per SM, plus the epilogue that no MMA covers.
-double pair_cost(long long tiles, int pairs, int kb, int mb, int nt) {
-  const double mma = 2.0 * mb * nt, load = (mb * 16384 + nt * 64) / 42.0;
-  return (double)((tiles + pairs - 1) / pairs) * (kb * (mma > load ? mma : load) + (mb * nt > 256 ? 3000.0 : 1000.0));
-}
-
-// Tilings of the CTA-pair kernel that are built for a product.
+// Tilings of the CTA-pair kernel that are built for a product, and the cycles
+// of its epilogue for a block of 256 columns.
 struct Tilings {
   int n;
   struct {
     int mb, nt;
   } t[4];
+  double epilogue;
 };
-constexpr Tilings kGluTilings{2, {{2, 256}, {2, 128}}};
-constexpr Tilings kDgluTilings{2, {{1, 256}, {1, 128}}};
-constexpr Tilings kStoreTilings{4, {{2, 256}, {2, 192}, {1, 256}, {1, 128}}};
-// one block: the scaling epilogue costs more than the B reads that two save (2011 x 5120 x 13824: 126 us
-// against 135)
-constexpr Tilings kI8Tilings{2, {{1, 256}, {1, 128}}};
+constexpr Tilings kGluTilings{2, {{2, 256}, {2, 128}}, 9000};
+constexpr Tilings kDgluTilings{2, {{1, 256}, {1, 128}}, 10000};
+constexpr Tilings kStoreTilings{4, {{2, 256}, {2, 192}, {1, 256}, {1, 128}}, 6000};
+constexpr Tilings kWeightTilings{2, {{2, 256}, {1, 256}}, 6000};
+constexpr Tilings kI8Tilings{2, {{1, 256}, {1, 128}}, 7000};
+
+// Estimated SM cycles of the two kernels.  A tiling's K blocks cost the slower
+// of the MMAs (2 cycles a column and block), the arrival of its bytes at the
+// SMs' share of the L2 (about 6 KB a cycle in all, 60 B at most for one SM) and,
+// for the split kernel, the latency of a load over the ring's depth.
+double pair_cost(long long tiles, int pairs, int kb, int mb, int nt, double epilogue, bool glu) {
+  const long long rounds = (tiles + pairs - 1) / pairs;
+  const double active = 2.0 * (tiles < pairs ? tiles : pairs);
+  const double rate = 6200.0 / active < 60.0 ? 6200.0 / active : 60.0;
+  const double mma = 2.0 * mb * nt, load = (mb * 16384 + nt * 64) / rate;
+  const double main = kb * (mma > load ? mma : load);
+  const double epi = epilogue * nt / 256.0 * (glu ? 1 : mb);
+  // two accumulator buffers: the epilogue of a tile runs under the next one's MMAs; one: about half of it does
+  const double body = mb * nt > 256 ? rounds * (main + 0.5 * epi) + 0.5 * epi
+                                    : rounds * (main > epi ? main : epi) + (main > epi ? epi : main);
+  return body + 5000.0;
+}
+// ntn: tiles along n, which share the weights that come from HBM (3450 B a
+// cycle in all, 19 B for one CTA: one token, 5120 x 13824, 108 tiles: 36 us
+// unsplit, 25.5 split by 2, 30.7 by 4, whose clusters take two rounds).
+double split_cost(long long tiles, int ntn, int kb, int nt, int split, int cap) {
+  const int ns = nt <= 16 ? 6 : nt <= 32 ? 5 : nt <= 64 ? 4 : 3;
+  const long long rounds = (tiles + cap - 1) / cap;
+  const double active = (double)(tiles < cap ? tiles : cap) * split, stage = 16384.0 + nt * 128.0;
+  const double hbm = 16384.0 / ntn / (3450.0 / active < 19.0 ? 3450.0 / active : 19.0);
+  const double load = stage * active / 6200.0, lat = 2200.0 / ns;
+  double per = load > lat ? load : lat;
+  if (hbm > per) per = hbm;
+  const double join = nt * 32.0 / split / GM::kSplitThreads * 180.0 + (split > 1 ? 800.0 : 0.0);
+  return rounds * ((double)((kb + split - 1) / split) * per + 2200.0 + join) + 3000.0;
+}
 
 // m_rows: features of a 128-row block (64 for the gate | up product).
 Plan choose(int m, int m_rows, int n, int kb, int sms, const Tilings &tilings) {
-  Plan p{};
-  p.mb = 1;
-  if (n <= 128) {
-    p.nt = n <= 16 ? 16 : n <= 32 ? 32 : n <= 64 ? 64 : 128;
-    p.split = true;
-    return p;
+  Plan best{};
+  double cost = 0;
+  const ClusterCaps *caps = cluster_caps();
+  if (!caps) return best;
+  const bool glu = m_rows == 64;
+  if (n > 128)
+    for (int i = 0; i < tilings.n; ++i) {
+      const auto &t = tilings.t[i];
+      const double c = pair_cost((long long)cdiv(m, 2 * t.mb * m_rows) * cdiv(n, t.nt), sms / 2, kb, t.mb, t.nt,
+                                 tilings.epilogue, glu);
+      if (cost == 0 || c < cost) cost = c, best = Plan{t.nt, t.mb, 0};
+    }
+  for (int nt = 16; nt <= 128; nt *= 2) {
+    const long long tiles = (long long)cdiv(m, m_rows) * cdiv(n, nt);
+    if (tiles > 65536) continue;
+    for (int split = 1; split <= kMaxSplit && (split == 1 || split * 4 <= kb); ++split) {
+      const int cap = caps->n[split];
+      // clusters of 3 and 7 leave SMs with one CTA where others have two: 333 tokens, 1032 x 2760 (66
+      // tiles) 15.5 us split by 3, 13.2 by 4; 40 tiles of K 13824 83.8 us by 7, 70.5 by 6
+      if (cap <= 0 || split == 3 || split == 7) continue;
+      const double c = split_cost(tiles, cdiv(n, nt), kb, nt, split, cap);
+      if (cost == 0 || c < cost) cost = c, best = Plan{nt, 1, split};
+    }
+    if (nt >= n) break;
   }
-  const int pairs = sms / 2;
-  const int pair_tiles = cdiv(m, 2 * m_rows) * cdiv(n, 128);
-  if (pair_tiles < pairs / 2) {
-    p.nt = 128;
-    p.split = true;
-    return p;
-  }
-  double best = 0;
-  for (int i = 0; i < tilings.n; ++i) {
-    const auto &t = tilings.t[i];
-    const double c = pair_cost((long long)cdiv(m, 2 * t.mb * m_rows) * cdiv(n, t.nt), pairs, kb, t.mb, t.nt);
-    if (i == 0 || c < best) best = c, p.mb = t.mb, p.nt = t.nt;
-  }
-  return p;
+  return best;
 }
 
 uint32_t idesc(int dtype, bool i8, int M, int N, int a_mn, int b_mn) {
@@ -171,6 +196,7 @@ uint32_t idesc(int dtype, bool i8, int M, int N, int a_mn, int b_mn) {
 
 template <int EPI, int AMN, typename T>
 cudaError_t run_plan(GM::Args &a, const Plan &p, int dtype, int m_rows, int sms, cudaStream_t st) {
+  if (!p.nt) return cudaErrorUnknown;
   a.mt = cdiv(a.m, p.split ? m_rows : 2 * p.mb * m_rows);
   a.nt = cdiv(a.n, p.nt);
   a.idesc = idesc(dtype, EPI == GM::E_I8, p.split ? 128 : 256, p.nt, AMN, 0);
@@ -190,13 +216,13 @@ cudaError_t run_plan(GM::Args &a, const Plan &p, int dtype, int m_rows, int sms,
   }
   switch (p.nt) {
   case 16:
-    return split_launch<EPI, AMN, 16, T>(a, st);
+    return split_launch<EPI, AMN, 16, T>(a, p.split, st);
   case 32:
-    return split_launch<EPI, AMN, 32, T>(a, st);
+    return split_launch<EPI, AMN, 32, T>(a, p.split, st);
   case 64:
-    return split_launch<EPI, AMN, 64, T>(a, st);
+    return split_launch<EPI, AMN, 64, T>(a, p.split, st);
   default:
-    return split_launch<EPI, AMN, 128, T>(a, st);
+    return split_launch<EPI, AMN, 128, T>(a, p.split, st);
   }
 }
 
@@ -308,10 +334,14 @@ pi_status ffn_backward(const pi_gated_ffn *h, const void *u, const void *gate, c
       a.out_type = grad_dtype;
       a.accumulate = acc;
       a.status = w.status;
-      const int mb = pair_cost((long long)a.nprob * cdiv(d, 512) * cdiv(f, 256), sms / 2, a.kb, 2, 256) <
-                             pair_cost((long long)a.nprob * cdiv(d, 256) * cdiv(f, 256), sms / 2, a.kb, 1, 256)
-                         ? 2
-                         : 1;
+      double best = 0;
+      int mb = 1;
+      for (int i = 0; i < kWeightTilings.n; ++i) {
+        const auto &t = kWeightTilings.t[i];
+        const double c = pair_cost((long long)a.nprob * cdiv(d, 256 * t.mb) * cdiv(f, t.nt), sms / 2, a.kb, t.mb, t.nt,
+                                   kWeightTilings.epilogue, false);
+        if (i == 0 || c < best) best = c, mb = t.mb;
+      }
       a.mt = cdiv(d, 256 * mb);
       a.nt = cdiv(f, 256);
       a.idesc = idesc(dt, false, 256, 256, 1, 1);
