@@ -337,27 +337,39 @@ def _check_out(t: Optional[torch.Tensor], what: str, dtype, shape):
 def _ptrs(names: str, *tensors: Optional[torch.Tensor]):
     """The tensors' addresses (None stays None).  All of them on the current
     CUDA device: kernels launch there, on its current stream."""
-    dev = -2
+    dev = None
     out = []
-    for k, t in enumerate(tensors):
+    for t in tensors:
         if t is None:
             out.append(None)
             continue
         d = t.get_device()
         if d != dev:
-            what = names.split()[k]
-            if d < 0:
-                raise ValueError(f"{what}: must be a CUDA tensor")
-            if d != torch.cuda.current_device():
-                raise ValueError(f"{what}: on {t.device}, but the current device is "
-                                 f"cuda:{torch.cuda.current_device()}")
-            dev = d
+            dev = _check_device(names, tensors, d)
         out.append(t.data_ptr())
     return out
 
 
+def _check_device(names: str, tensors, d: int) -> int:
+    """Device d of one of the tensors, if it is the current one."""
+    if d < 0 or d != torch.cuda.current_device():
+        what, t = next((w, t) for w, t in zip(names.split(), tensors) if t is not None and t.get_device() == d)
+        if d < 0:
+            raise ValueError(f"{what}: must be a CUDA tensor")
+        raise ValueError(f"{what}: on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
+    return d
+
+
+# the current stream's handle without building a Stream object (3 us a call), where torch has it
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _raw_stream(stream):
-    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    if _current_raw_stream is not None:
+        return _current_raw_stream(torch.cuda.current_device())
+    return torch.cuda.current_stream().cuda_stream
 
 
 def _ws_bytes(ws: torch.Tensor) -> int:

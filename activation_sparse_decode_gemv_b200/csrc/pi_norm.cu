@@ -20,32 +20,38 @@ constexpr int kMaxI8K = 131056;
 
 // ---------------------------------------------------------------- norms
 // Launch shape of the row kernels: up to 512 threads with ch chunks of 4
-// elements each, a ring of `rows` rows in shared memory (one row, refilled
-// once it is in registers, where two do not fit), `per_sm` blocks per SM.
+// elements each; rows over 8192 elements by clusters of two blocks; a ring of
+// `rows` rows in shared memory (one row, refilled once it is in registers,
+// where two do not fit); `per_sm` blocks per SM.
 struct RowShape {
   int threads, ch, rows, per_sm;
+  bool cluster;
   size_t smem;
 };
-constexpr size_t kRowSmem = 200 * 1024;  // of the 227 KB per block; the rest is L1 for the column factors
+constexpr int kRowBlocks = 8;               // blocks per SM of the backward kernel, at most
+constexpr size_t kRowSmem = 200 * 1024;     // of the 227 KB per block; the rest is L1 for the column factors
 RowShape row_shape(int d, int bytes_per_element, bool backward) {
-  const int chunks = d / 4;
   RowShape r{};
-  r.ch = cdiv(chunks, 512);
-  if (r.ch > 4) r.ch = 8;
+  r.cluster = d > 8192;
+  const int chunks = (r.cluster ? d / 2 : d) / 4;
+  // short rows: one warp each, without block barriers (16384 x 448 forward 17.1 us against 23.1)
+  r.ch = chunks <= 128 ? cdiv(chunks, 32) : cdiv(chunks, 512);
   r.threads = cdiv(cdiv(chunks, r.ch), 32) * 32;
   const size_t row = (size_t)r.threads * r.ch * 4 * bytes_per_element;
   r.rows = 2 * row <= kRowSmem ? 2 : 1;
   r.smem = r.rows * row;
   r.per_sm = (int)(kRowSmem / (r.smem + 1024));
-  // threads that the registers hold: forward up to 38, 64, 64, 115, 128 a thread
-  // for ch = 1, 2, 3, 4, 8; backward 98, 102, 126, 128
+  // threads that the registers hold: forward up to 38, 64, 64, 115 a thread for
+  // ch = 1, 2, 3, 4; backward 98, 102, 126, 128
   const int fits = r.ch > 3 ? 512 : backward ? (r.ch == 1 ? 640 : r.ch == 2 ? 608 : 512) : r.ch == 1 ? 1536 : 1024;
   const int by_threads = fits / r.threads;
   if (r.per_sm > by_threads) r.per_sm = by_threads;
   if (r.per_sm < 1) r.per_sm = 1;
-  if (r.per_sm > 16) r.per_sm = 16;
+  if (r.per_sm > (backward ? kRowBlocks : 16)) r.per_sm = backward ? kRowBlocks : 16;
   return r;
 }
+// Row groups (blocks, or clusters of two) that the machine holds.
+int row_groups(const RowShape &r, int sms) { return sms * r.per_sm / (r.cluster ? 2 : 1); }
 pi_status check_norm(const pi_block_norm_desc *D) {
   if (!D || D->d_model <= 0 || !is_type(D->y_dtype) || !is_type(D->u_dtype)) return PI_ERR_INVALID_ARG;
   if (!(D->eps > 0.f) || !std::isfinite(D->eps) || !std::isfinite(D->residual_scale) || !std::isfinite(D->branch_scale))
@@ -57,41 +63,67 @@ pi_status check_norm(const pi_block_norm_desc *D) {
     return PI_ERR_MISALIGNED;
   return PI_OK;
 }
-// Blocks of the backward kernel: enough to fill the machine, but four rows
-// each where the tokens allow, since a block leaves a row of partials behind.
-// At most kBwdBlocks per SM whatever the types, so that a workspace sized for
-// more tokens serves fewer.
-constexpr int kBwdBlocks = 8;
-int norm_bwd_blocks(int per_sm, int tokens, int sms) {
-  if (per_sm > kBwdBlocks) per_sm = kBwdBlocks;
+// Row groups of the backward kernel: enough to fill the machine, but four rows
+// each where the tokens allow, since a group leaves a row of partials behind.
+// `most` is at most kRowBlocks per SM whatever the types, so that a workspace
+// sized for more tokens serves fewer.
+int norm_bwd_groups(int most, int tokens, int sms) {
   int g = cdiv(tokens, 4);
   if (g < sms) g = sms;
-  if (g > sms * per_sm) g = sms * per_sm;
-  if (g > NM::kMaxBwdBlocks) g = NM::kMaxBwdBlocks;
+  if (g > most) g = most;
   return tokens < g ? tokens : g;
 }
-// types: 3 * y + u
-template <int CH, int R>
-pi_status fwd_launch(const NM::FwdArgs &a, dim3 g, const RowShape &r, cudaStream_t st) {
-  static void (*const kern[9])(NM::FwdArgs) = {
-      NM::norm_fwd_kernel<CH, R, 0, 0>, NM::norm_fwd_kernel<CH, R, 0, 1>, NM::norm_fwd_kernel<CH, R, 0, 2>,
-      NM::norm_fwd_kernel<CH, R, 1, 0>, NM::norm_fwd_kernel<CH, R, 1, 1>, NM::norm_fwd_kernel<CH, R, 1, 2>,
-      NM::norm_fwd_kernel<CH, R, 2, 0>, NM::norm_fwd_kernel<CH, R, 2, 1>, NM::norm_fwd_kernel<CH, R, 2, 2>};
+template <int CH, int R, bool CL>
+pi_status fwd_launch(const NM::FwdArgs &a, int groups, const RowShape &r, cudaStream_t st) {
+  static void (*const kern[9])(NM::FwdArgs) = {  // 3 * y type + u type
+      NM::norm_fwd_kernel<CH, R, CL, 0, 0>, NM::norm_fwd_kernel<CH, R, CL, 0, 1>, NM::norm_fwd_kernel<CH, R, CL, 0, 2>,
+      NM::norm_fwd_kernel<CH, R, CL, 1, 0>, NM::norm_fwd_kernel<CH, R, CL, 1, 1>, NM::norm_fwd_kernel<CH, R, CL, 1, 2>,
+      NM::norm_fwd_kernel<CH, R, CL, 2, 0>, NM::norm_fwd_kernel<CH, R, CL, 2, 1>, NM::norm_fwd_kernel<CH, R, CL, 2, 2>};
   static DeviceOnce once[9];
   const int k = 3 * a.y_type + a.u_type;
-  PI_CUDA(launch1(kern[k], g, r.threads, r.smem, 0, &once[k], st, a));
+  PI_CUDA(launch1(kern[k], dim3(groups * (CL ? 2 : 1)), r.threads, r.smem, CL ? 2 : 0, &once[k], st, a));
   return PI_OK;
 }
-template <int CH, int R>
-pi_status bwd_launch(const NM::BwdArgs &a, int G, const RowShape &r, cudaStream_t st) {
+template <int CH, int R, bool CL>
+pi_status bwd_launch(const NM::BwdArgs &a, int groups, const RowShape &r, cudaStream_t st) {
   static void (*const kern[9])(NM::BwdArgs) = {
-      NM::norm_bwd_kernel<CH, R, 0, 0>, NM::norm_bwd_kernel<CH, R, 0, 1>, NM::norm_bwd_kernel<CH, R, 0, 2>,
-      NM::norm_bwd_kernel<CH, R, 1, 0>, NM::norm_bwd_kernel<CH, R, 1, 1>, NM::norm_bwd_kernel<CH, R, 1, 2>,
-      NM::norm_bwd_kernel<CH, R, 2, 0>, NM::norm_bwd_kernel<CH, R, 2, 1>, NM::norm_bwd_kernel<CH, R, 2, 2>};
+      NM::norm_bwd_kernel<CH, R, CL, 0, 0>, NM::norm_bwd_kernel<CH, R, CL, 0, 1>, NM::norm_bwd_kernel<CH, R, CL, 0, 2>,
+      NM::norm_bwd_kernel<CH, R, CL, 1, 0>, NM::norm_bwd_kernel<CH, R, CL, 1, 1>, NM::norm_bwd_kernel<CH, R, CL, 1, 2>,
+      NM::norm_bwd_kernel<CH, R, CL, 2, 0>, NM::norm_bwd_kernel<CH, R, CL, 2, 1>, NM::norm_bwd_kernel<CH, R, CL, 2, 2>};
   static DeviceOnce once[9];
   const int k = 3 * a.y_type + a.u_type;
-  PI_CUDA(launch1(kern[k], dim3(G), r.threads, r.smem, 0, &once[k], st, a));
+  PI_CUDA(launch1(kern[k], dim3(groups * (CL ? 2 : 1)), r.threads, r.smem, CL ? 2 : 0, &once[k], st, a));
   return PI_OK;
+}
+// Clusters have ch 3 or 4; only the backward kernel's rows of ch = 4 can exceed a ring of two.
+pi_status fwd_dispatch(const NM::FwdArgs &a, int groups, const RowShape &r, cudaStream_t st) {
+  if (r.cluster) return r.ch == 3 ? fwd_launch<3, 2, true>(a, groups, r, st) : fwd_launch<4, 2, true>(a, groups, r, st);
+  switch (r.ch) {
+  case 1:
+    return fwd_launch<1, 2, false>(a, groups, r, st);
+  case 2:
+    return fwd_launch<2, 2, false>(a, groups, r, st);
+  case 3:
+    return fwd_launch<3, 2, false>(a, groups, r, st);
+  default:
+    return fwd_launch<4, 2, false>(a, groups, r, st);
+  }
+}
+pi_status bwd_dispatch(const NM::BwdArgs &a, int groups, const RowShape &r, cudaStream_t st) {
+  if (r.cluster)
+    return r.ch == 3     ? bwd_launch<3, 2, true>(a, groups, r, st)
+           : r.rows == 2 ? bwd_launch<4, 2, true>(a, groups, r, st)
+                         : bwd_launch<4, 1, true>(a, groups, r, st);
+  switch (r.ch) {
+  case 1:
+    return bwd_launch<1, 2, false>(a, groups, r, st);
+  case 2:
+    return bwd_launch<2, 2, false>(a, groups, r, st);
+  case 3:
+    return bwd_launch<3, 2, false>(a, groups, r, st);
+  default:
+    return r.rows == 2 ? bwd_launch<4, 2, false>(a, groups, r, st) : bwd_launch<4, 1, false>(a, groups, r, st);
+  }
 }
 size_t norm_ws_bytes(int d, int G) { return kHeader + (size_t)G * d * 4 * 4; }  // dw_post, dw_pre, 2 gate rows
 
@@ -127,22 +159,8 @@ pi_status pi_block_norm_forward(const pi_block_norm_desc *desc, const float *x, 
   const int sms = device_sm_count();
   if (sms <= 0) return PI_ERR_CUDA;
   const RowShape r = row_shape(a.d, 4 + (int)type_size(desc->y_dtype), false);
-  const dim3 g(tokens < sms * r.per_sm ? tokens : sms * r.per_sm);
-  cudaStream_t st = (cudaStream_t)stream;
-  switch (r.ch * 2 + r.rows) {
-  case 4:
-    return fwd_launch<1, 2>(a, g, r, st);
-  case 6:
-    return fwd_launch<2, 2>(a, g, r, st);
-  case 8:
-    return fwd_launch<3, 2>(a, g, r, st);
-  case 10:
-    return fwd_launch<4, 2>(a, g, r, st);
-  case 18:
-    return fwd_launch<8, 2>(a, g, r, st);
-  default:
-    return fwd_launch<8, 1>(a, g, r, st);
-  }
+  const int most = row_groups(r, sms), groups = tokens < most ? tokens : most;
+  return fwd_dispatch(a, groups, r, (cudaStream_t)stream);
 }
 
 pi_status pi_block_norm_workspace_size(const pi_block_norm_desc *desc, int max_tokens, size_t *bytes) {
@@ -152,7 +170,7 @@ pi_status pi_block_norm_workspace_size(const pi_block_norm_desc *desc, int max_t
   if (max_tokens < 0 || max_tokens > kMaxTokens) return PI_ERR_UNSUPPORTED;
   const int sms = device_sm_count();
   if (sms <= 0) return PI_ERR_CUDA;
-  *bytes = norm_ws_bytes(desc->d_model, norm_bwd_blocks(kBwdBlocks, max_tokens, sms));
+  *bytes = norm_ws_bytes(desc->d_model, norm_bwd_groups(sms * kRowBlocks, max_tokens, sms));
   return PI_OK;
 }
 
@@ -191,7 +209,7 @@ pi_status pi_block_norm_backward(const pi_block_norm_desc *desc, const float *x_
   const int sms = device_sm_count();
   if (sms <= 0) return PI_ERR_CUDA;
   const RowShape r = row_shape(d, 8 + (int)type_size(desc->u_dtype) + (int)type_size(desc->y_dtype), true);
-  const int G = norm_bwd_blocks(r.ch > 4 ? 1 : r.per_sm, tokens, sms);
+  const int G = norm_bwd_groups(row_groups(r, sms), tokens, sms);
   if (ws_bytes < norm_ws_bytes(d, G)) return PI_ERR_WORKSPACE;
   float *part = reinterpret_cast<float *>(static_cast<char *>(ws) + kHeader);
   NM::BwdArgs a{};
@@ -205,27 +223,7 @@ pi_status pi_block_norm_backward(const pi_block_norm_desc *desc, const float *x_
   a.y_type = desc->y_dtype, a.u_type = desc->u_dtype, a.post_norm = desc->post_norm ? 1 : 0;
   a.accumulate = acc;
   a.alpha = desc->residual_scale, a.beta = desc->branch_scale;
-  switch (r.ch * 2 + r.rows) {
-  case 4:
-    s = bwd_launch<1, 2>(a, G, r, st);
-    break;
-  case 6:
-    s = bwd_launch<2, 2>(a, G, r, st);
-    break;
-  case 8:
-    s = bwd_launch<3, 2>(a, G, r, st);
-    break;
-  case 9:
-    s = bwd_launch<4, 1>(a, G, r, st);
-    break;
-  case 10:
-    s = bwd_launch<4, 2>(a, G, r, st);
-    break;
-  default: {
-    static DeviceOnce once;
-    PI_CUDA(launch1(NM::norm_bwd_wide_kernel, dim3(G), 1024, (size_t)d * 8, 0, &once, st, a));
-  }
-  }
+  s = bwd_dispatch(a, G, r, st);
   if (s != PI_OK) return s;
   if (dw_post || dw_pre || dgate) {
     NM::JoinArgs j{};
@@ -238,7 +236,8 @@ pi_status pi_block_norm_backward(const pi_block_norm_desc *desc, const float *x_
       j.gate_jobs = j.long_rows ? rows : rows < NM::kGateJobs ? rows : NM::kGateJobs;
     }
     const dim3 g(cdiv(d, 32), 2 + j.gate_jobs);
-    PI_CUDA(launch1(NM::norm_join_kernel, g, 256, 0, 0, nullptr, st, j));
+    // more warps where there are few columns and many partial rows
+    PI_CUDA(launch1(NM::norm_join_kernel, g, G > 256 ? 1024 : 256, 0, 0, nullptr, st, j));
   }
   return PI_OK;
 }

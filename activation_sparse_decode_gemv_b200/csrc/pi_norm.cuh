@@ -50,13 +50,50 @@ PI_DEV float dot4(float4 a, float4 b) { return fmaf(a.w, b.w, fmaf(a.z, b.z, fma
 PI_DEV float4 one4() { return make_float4(1.f, 1.f, 1.f, 1.f); }
 PI_DEV float4 zero4() { return make_float4(0.f, 0.f, 0.f, 0.f); }
 
-// Block-wide sums of N values; buf: 32 N floats of shared memory that no warp
+// A row is summed by one block, or by a cluster of two blocks with half of its
+// columns each (CL; rows over 8192 elements, whose values and column sums do
+// not fit one block's registers).  The blocks of a cluster exchange their
+// warps' sums through each other's shared memory.
+template <bool CL>
+PI_DEV int cluster_half() {
+  if constexpr (!CL) return 0;
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return (int)r;
+}
+template <bool CL>
+PI_DEV void row_sync() {
+  if constexpr (CL) {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  } else {
+    __syncthreads();
+  }
+}
+// Row-wide sums of N values; buf: 32 N floats of shared memory that no warp
 // has read since the last but one barrier (callers alternate two buffers).
-template <int N>
-PI_DEV void block_sum(float (&v)[N], float *buf) {
+template <int N, bool CL>
+PI_DEV void row_sum(float (&v)[N], float *buf) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
 #pragma unroll
   for (int k = 0; k < N; ++k) v[k] = warp_sum(v[k]);
+  if constexpr (CL) {
+    const int half = cluster_half<CL>();
+    if (lane == 0) {
+      const uint32_t at = (uint32_t)__cvta_generic_to_shared(buf + half * 16 + warp);
+      uint32_t peer;
+      asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(peer) : "r"(at), "r"(half ^ 1));
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+        buf[k * 32 + half * 16 + warp] = v[k];
+        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(peer + k * 128), "f"(v[k]) : "memory");
+      }
+    }
+    row_sync<CL>();
+#pragma unroll
+    for (int k = 0; k < N; ++k) v[k] = warp_sum((lane & 15) < nw ? buf[k * 32 + lane] : 0.f);
+    return;
+  }
   if (nw == 1) return;
   if (lane == 0)
 #pragma unroll
@@ -169,11 +206,12 @@ PI_DEV unsigned valid_chunks(int d) {
   for (int c = 0; c < CH; ++c) v |= (unsigned)((int)(threadIdx.x + c * blockDim.x) * 4 < d) << c;
   return v;
 }
-PI_DEV const void *row_at(const void *p, int t, int d, int type) {
-  return static_cast<const char *>(p) + (size_t)t * d * (type == T_F32 ? 4 : 2);
+// element col of row t
+PI_DEV const void *row_at(const void *p, int t, int d, int col, int type) {
+  return static_cast<const char *>(p) + ((size_t)t * d + col) * (type == T_F32 ? 4 : 2);
 }
-PI_DEV void *row_at(void *p, int t, int d, int type) {
-  return static_cast<char *>(p) + (size_t)t * d * (type == T_F32 ? 4 : 2);
+PI_DEV void *row_at(void *p, int t, int d, int col, int type) {
+  return static_cast<char *>(p) + ((size_t)t * d + col) * (type == T_F32 ? 4 : 2);
 }
 
 // First of the rows that block c of G takes: contiguous runs of equal length.
@@ -204,19 +242,20 @@ PI_DEV float4 branch_factor(const float *gate_row, const float *w_post, float be
 
 // One block per run of rows; a row stays in registers between its two block
 // sums.  Bound by HBM: 4 + |y| bytes read and 4 + |u| written per element.
-// The column factors stay in registers too where they fit (CH <= 4).
-template <int CH, int R, int YT, int UT>
+// The column factors stay in registers too.
+template <int CH, int R, bool CL, int YT, int UT>
 __global__ void __launch_bounds__(512, CH <= 3 ? 2 : 1) norm_fwd_kernel(const FwdArgs a) {
-  constexpr bool KEEP = CH <= 4;
   using X = Part<CH, T_F32>;
   using Y = Part<CH, YT>;
   using U = Part<CH, UT>;
   extern __shared__ __align__(16) unsigned char ring[];
   __shared__ float buf[2][32];
-  const int d = a.d, step = blockDim.x, G = gridDim.x;
-  const int t0 = first_token(a.tokens, G, blockIdx.x), t1 = first_token(a.tokens, G, blockIdx.x + 1);
+  const int d = a.d, step = blockDim.x, half = cluster_half<CL>();
+  const int dh = CL ? d / 2 : d, col0 = half * dh;  // this block's columns
+  const int G = gridDim.x / (CL ? 2 : 1), blk = blockIdx.x / (CL ? 2 : 1);
+  const int t0 = first_token(a.tokens, G, blk), t1 = first_token(a.tokens, G, blk + 1);
   const float inv_d = 1.f / (float)d;
-  const unsigned valid = valid_chunks<CH>(d);
+  const unsigned valid = valid_chunks<CH>(dh);
   const int xb = CH * step * 16, slot_b = xb + CH * step * Y::B;
   const uint32_t ring_s = (uint32_t)__cvta_generic_to_shared(ring);
 #pragma unroll
@@ -226,8 +265,8 @@ __global__ void __launch_bounds__(512, CH <= 3 ? 2 : 1) norm_fwd_kernel(const Fw
   }
   auto fetch = [&](int t, int k) {  // row t into slot k
     if (t < t1) {
-      X::fetch(ring_s + k * slot_b, row_at(a.x, t, d, T_F32), step, valid);
-      if (a.y) Y::fetch(ring_s + k * slot_b + xb, row_at(a.y, t, d, YT), step, valid);
+      X::fetch(ring_s + k * slot_b, row_at(a.x, t, d, col0, T_F32), step, valid);
+      if (a.y) Y::fetch(ring_s + k * slot_b + xb, row_at(a.y, t, d, col0, YT), step, valid);
     }
     cp_commit();
   };
@@ -235,32 +274,24 @@ __global__ void __launch_bounds__(512, CH <= 3 ? 2 : 1) norm_fwd_kernel(const Fw
   pdl_launch_dependents();
 #pragma unroll
   for (int k = 0; k < R; ++k) fetch(t0 + k, k);
+  auto col = [&](int c) { return col0 + (int)(threadIdx.x + c * step) * 4; };
   auto factor = [&](const float *gate_row, int c) {
-    return valid >> c & 1u ? p4(branch_factor(gate_row, a.w_post, a.beta, (threadIdx.x + c * step) * 4)) : p4(zero4());
-  };
-  auto weight = [&](int c) {
-    return a.w_pre && (valid >> c & 1u) ? p4(ld4(a.w_pre + (threadIdx.x + c * step) * 4)) : p4(one4());
+    return valid >> c & 1u ? p4(branch_factor(gate_row, a.w_post, a.beta, col(c))) : p4(zero4());
   };
   int group = -1;
-  const float *gate_row = nullptr;
-  P4 bf[KEEP ? CH : 1], wp[KEEP ? CH : 1];
-  if constexpr (KEEP) {
+  P4 bf[CH], wp[CH];
 #pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      wp[c] = weight(c);
-      if (!a.gate) bf[c] = factor(nullptr, c);
-    }
+  for (int c = 0; c < CH; ++c) {
+    wp[c] = a.w_pre && (valid >> c & 1u) ? p4(ld4(a.w_pre + col(c))) : p4(one4());
+    if (!a.gate) bf[c] = factor(nullptr, c);
   }
   const unsigned long long alpha = pk(a.alpha, a.alpha);
   int slot_i = 0;
   for (int t = t0; t < t1; ++t) {
     if (a.gate && t / a.tokens_per_gate != group) {
       group = t / a.tokens_per_gate;
-      gate_row = a.gate + (size_t)group * d;
-      if constexpr (KEEP) {
 #pragma unroll
-        for (int c = 0; c < CH; ++c) bf[c] = factor(gate_row, c);
-      }
+      for (int c = 0; c < CH; ++c) bf[c] = factor(a.gate + (size_t)group * d, c);
     }
     cp_wait<R - 1>();
     const unsigned char *slot = ring + slot_i * slot_b;
@@ -277,43 +308,38 @@ __global__ void __launch_bounds__(512, CH <= 3 ? 2 : 1) norm_fwd_kernel(const Fw
     float rp = 1.f;
     if (a.post_norm) {
       float s[1] = {sum2(q)};
-      block_sum(s, buf[0]);
+      row_sum<1, CL>(s, buf[0]);
       rp = rsqrtf(s[0] * inv_d + a.eps);
-      if (a.rstd_post && threadIdx.x == 0) a.rstd_post[t] = rp;
+      if (a.rstd_post && threadIdx.x == 0 && half == 0) a.rstd_post[t] = rp;
     }
     const unsigned long long rp2 = pk(rp, rp);
     q = 0;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      P4 f;
-      if constexpr (KEEP) f = bf[c];
-      else f = factor(gate_row, c);
-      r[c] = fma(mul(rp2, y[c]), f, r[c]);
+      r[c] = fma(mul(rp2, y[c]), bf[c], r[c]);
       q = dot(r[c], r[c], q);
     }
     if (a.x_out) {
-      void *o = row_at(a.x_out, t, d, T_F32);
+      void *o = row_at(a.x_out, t, d, col0, T_F32);
 #pragma unroll
       for (int c = 0; c < CH; ++c)
         if (valid >> c & 1u) X::store(o, c, step, r[c]);
     }
     if (a.u) {
       float s[1] = {sum2(q)};
-      block_sum(s, buf[1]);
+      row_sum<1, CL>(s, buf[1]);
       const float rr = rsqrtf(s[0] * inv_d + a.eps);
-      if (a.rstd_pre && threadIdx.x == 0) a.rstd_pre[t] = rr;
+      if (a.rstd_pre && threadIdx.x == 0 && half == 0) a.rstd_pre[t] = rr;
       const unsigned long long rr2 = pk(rr, rr);
-      void *o = row_at(a.u, t, d, UT);
+      void *o = row_at(a.u, t, d, col0, UT);
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
-        P4 w;
-        if constexpr (KEEP) w = wp[c];
-        else w = weight(c);
-        if (valid >> c & 1u) U::store(o, c, step, mul(mul(rr2, r[c]), w));
+        if (valid >> c & 1u) U::store(o, c, step, mul(mul(rr2, r[c]), wp[c]));
       }
     }
-    if (!(a.post_norm && a.u)) __syncthreads();  // one buffer in use: keep rows apart
+    if (!(a.post_norm && a.u)) row_sync<CL>();  // one buffer in use: keep rows apart
   }
+  if constexpr (CL) row_sync<CL>();  // the other block has written its last sums
 }
 
 // ---------------------------------------------------------------- backward
@@ -343,12 +369,12 @@ struct BwdArgs {
 // At the end of the tokens of gate row `group` (or of the block's rows): adds
 // beta gate S to the block's dw_post sums and stores the gate's gradient, for
 // the 4 columns at i.  post0: nothing is in part_post yet.
-PI_DEV void flush_gate(const BwdArgs &a, int group, int group0, int t0, int t1, int i, float4 S, bool post0) {
+PI_DEV void flush_gate(const BwdArgs &a, int blk, int group, int group0, int t0, int t1, int i, float4 S, bool post0) {
   const float *grow = a.gate ? a.gate + (size_t)group * a.d : nullptr;
   if (a.part_post) {
     float4 v = scale4(a.beta, S);
     if (grow) v = mul4(v, ld4(grow + i));
-    float *dst = a.part_post + (size_t)blockIdx.x * a.d + i;
+    float *dst = a.part_post + (size_t)blk * a.d + i;
     if (!post0) v = add4(v, ld4(dst));
     *reinterpret_cast<float4 *>(dst) = v;
   }
@@ -360,7 +386,7 @@ PI_DEV void flush_gate(const BwdArgs &a, int group, int group0, int t0, int t1, 
     float4 v = scale4(a.beta, S);
     if (a.w_post) v = mul4(v, ld4(a.w_post + i));
     float *dst = (whole ? a.dgate + (size_t)group * a.d
-                        : a.part_gate + ((size_t)blockIdx.x * 2 + (group != group0)) * a.d) + i;
+                        : a.part_gate + ((size_t)blk * 2 + (group != group0)) * a.d) + i;
     if (whole && a.accumulate) v = add4(v, ld4(dst));
     *reinterpret_cast<float4 *>(dst) = v;
   }
@@ -369,17 +395,19 @@ PI_DEV void flush_gate(const BwdArgs &a, int group, int group0, int t0, int t1, 
 // One block per run of rows (CH <= 4 chunks a thread).  Column sums stay in
 // registers, dw_post's in the block's own row of partials, so every order is
 // fixed.  A tensor that is not given has zeros in its part of the ring.
-template <int CH, int R, int YT, int UT>
+template <int CH, int R, bool CL, int YT, int UT>
 __global__ void __launch_bounds__(512) norm_bwd_kernel(const BwdArgs a) {
   using X = Part<CH, T_F32>;
   using Y = Part<CH, YT>;
   using U = Part<CH, UT>;
   extern __shared__ __align__(16) unsigned char ring[];
   __shared__ float buf[2][96];
-  const int d = a.d, step = blockDim.x, G = gridDim.x;
-  const int t0 = first_token(a.tokens, G, blockIdx.x), t1 = first_token(a.tokens, G, blockIdx.x + 1);
+  const int d = a.d, step = blockDim.x, half = cluster_half<CL>();
+  const int dh = CL ? d / 2 : d, col0 = half * dh;  // this block's columns
+  const int G = gridDim.x / (CL ? 2 : 1), blk = blockIdx.x / (CL ? 2 : 1);
+  const int t0 = first_token(a.tokens, G, blk), t1 = first_token(a.tokens, G, blk + 1);
   const float inv_d = 1.f / (float)d;
-  const unsigned valid = valid_chunks<CH>(d);
+  const unsigned valid = valid_chunks<CH>(dh);
   const int o_g = CH * step * 16, o_u = 2 * o_g, o_y = o_u + CH * step * U::B, slot_b = o_y + CH * step * Y::B;
   const uint32_t ring_s = (uint32_t)__cvta_generic_to_shared(ring);
 #pragma unroll
@@ -394,11 +422,11 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const BwdArgs a) {
     if (t < t1) {
       const uint32_t slot = ring_s + k * slot_b;
       if (a.du) {
-        X::fetch(slot, row_at(a.x_out, t, d, T_F32), step, valid);
-        U::fetch(slot + o_u, row_at(a.du, t, d, UT), step, valid);
+        X::fetch(slot, row_at(a.x_out, t, d, col0, T_F32), step, valid);
+        U::fetch(slot + o_u, row_at(a.du, t, d, col0, UT), step, valid);
       }
-      if (a.dx_out) X::fetch(slot + o_g, row_at(a.dx_out, t, d, T_F32), step, valid);
-      if (a.y) Y::fetch(slot + o_y, row_at(a.y, t, d, YT), step, valid);
+      if (a.dx_out) X::fetch(slot + o_g, row_at(a.dx_out, t, d, col0, T_F32), step, valid);
+      if (a.y) Y::fetch(slot + o_y, row_at(a.y, t, d, col0, YT), step, valid);
     }
     cp_commit();
   };
@@ -409,8 +437,9 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const BwdArgs a) {
   const bool post = a.y && a.post_norm;
   auto rr_of = [&](int t) { return a.du ? __ldg(a.rstd_pre + t) : 0.f; };
   auto rp_of = [&](int t) { return post ? __ldg(a.rstd_post + t) : 1.f; };
+  auto col = [&](int c) { return col0 + (int)(threadIdx.x + c * step) * 4; };
   auto factor = [&](const float *gate_row, int c) {
-    return valid >> c & 1u ? p4(branch_factor(gate_row, a.w_post, a.beta, (threadIdx.x + c * step) * 4)) : p4(zero4());
+    return valid >> c & 1u ? p4(branch_factor(gate_row, a.w_post, a.beta, col(c))) : p4(zero4());
   };
   P4 s_pre[CH], S[CH], bf[CH];
   int group = a.gate ? t0 / a.tokens_per_gate : 0;
@@ -424,7 +453,7 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const BwdArgs a) {
   auto flush = [&]() {
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      if (valid >> c & 1u) flush_gate(a, group, group0, t0, t1, (threadIdx.x + c * step) * 4, f4(S[c]), post0);
+      if (valid >> c & 1u) flush_gate(a, blk, group, group0, t0, t1, col(c), f4(S[c]), post0);
       S[c] = p4(zero4());
     }
     post0 = false;
@@ -455,7 +484,7 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const BwdArgs a) {
       m[c] = mul(rp2, Y::load(slot + o_y, c, step));
       P4 v = U::load(slot + o_u, c, step);
       s_pre[c] = fma(v, n[c], s_pre[c]);
-      if (a.w_pre && (valid >> c & 1u)) v = mul(v, p4(ld4(a.w_pre + (threadIdx.x + c * step) * 4)));
+      if (a.w_pre && (valid >> c & 1u)) v = mul(v, p4(ld4(a.w_pre + col(c))));
       q0 = dot(v, n[c], q0);
       dr[c] = fma(rr2, v, X::load(slot + o_g, c, step));  // dr without the term of c
       const P4 q = mul(bf[c], m[c]);
@@ -465,11 +494,11 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const BwdArgs a) {
     fetch(t + R, slot_i);
     if (++slot_i == R) slot_i = 0;
     float s[3] = {sum2(q0), sum2(q1), sum2(q2)};
-    block_sum(s, buf[t & 1]);
+    row_sum<3, CL>(s, buf[t & 1]);
     const float cd = rr * s[0] * inv_d;                         // dr -= cd n
     const float ed = post ? (s[1] - cd * s[2]) * inv_d : 0.f;   // dy = rp (f dr - ed m)
     const unsigned long long cd2 = pk(-cd, -cd), ed2 = pk(-ed, -ed);
-    void *dx = a.dx ? row_at(a.dx, t, d, T_F32) : nullptr, *dy = a.dy ? row_at(a.dy, t, d, YT) : nullptr;
+    void *dx = a.dx ? row_at(a.dx, t, d, col0, T_F32) : nullptr, *dy = a.dy ? row_at(a.dy, t, d, col0, YT) : nullptr;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       const P4 d4 = fma(cd2, n[c], dr[c]);
@@ -485,87 +514,8 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const BwdArgs a) {
 #pragma unroll
   for (int c = 0; c < CH; ++c)
     if (a.part_pre && (valid >> c & 1u))
-      *reinterpret_cast<float4 *>(a.part_pre + (size_t)blockIdx.x * d + (threadIdx.x + c * step) * 4) = f4(s_pre[c]);
-}
-
-// The same for rows whose values and column sums exceed the registers (d >
-// 8192): a row is read twice, the second time from L2, and the column sums
-// live in shared memory ([2 x d]: dw_pre's and S).
-__global__ void __launch_bounds__(1024) norm_bwd_wide_kernel(const BwdArgs a) {
-  extern __shared__ __align__(16) unsigned char ring[];
-  __shared__ float buf[2][96];
-  pdl_wait();
-  pdl_launch_dependents();
-  float *s_pre = reinterpret_cast<float *>(ring), *S = s_pre + a.d;
-  const int G = gridDim.x;
-  const int t0 = first_token(a.tokens, G, blockIdx.x), t1 = first_token(a.tokens, G, blockIdx.x + 1);
-  const float inv_d = 1.f / (float)a.d;
-  const int step = blockDim.x * 4, i0 = threadIdx.x * 4;
-  for (int i = i0; i < a.d; i += step) {
-    *reinterpret_cast<float4 *>(s_pre + i) = zero4();
-    *reinterpret_cast<float4 *>(S + i) = zero4();
-  }
-  int group = a.gate ? t0 / a.tokens_per_gate : 0;
-  const int group0 = group;
-  bool post0 = true;
-  auto flush = [&]() {
-    for (int i = i0; i < a.d; i += step) {
-      flush_gate(a, group, group0, t0, t1, i, ld4(S + i), post0);
-      *reinterpret_cast<float4 *>(S + i) = zero4();
-    }
-    post0 = false;
-  };
-  for (int t = t0; t < t1; ++t) {
-    const size_t row = (size_t)t * a.d;
-    if (a.gate && t / a.tokens_per_gate != group) {
-      flush();
-      group = t / a.tokens_per_gate;
-    }
-    const float *grow = a.gate ? a.gate + (size_t)group * a.d : nullptr;
-    const float rr = a.du ? a.rstd_pre[t] : 0.f;
-    const float rp = a.y && a.post_norm ? a.rstd_post[t] : 1.f;
-    auto load = [&](int i, float4 &n, float4 &v, float4 &m, float4 &dr) {
-      n = v = m = dr = zero4();
-      if (a.dx_out) dr = ld4(a.dx_out + row + i);
-      if (a.y) m = scale4(rp, ld4(a.y, row + i, a.y_type));
-      if (a.du) {
-        n = scale4(rr, ld4(a.x_out + row + i));
-        v = ld4(a.du, row + i, a.u_type);
-      }
-    };
-    float s[3] = {0.f, 0.f, 0.f};
-#pragma unroll 2
-    for (int i = i0; i < a.d; i += step) {
-      float4 n, v, m, dr;
-      load(i, n, v, m, dr);
-      if (a.w_pre) v = mul4(v, ld4(a.w_pre + i));
-      s[0] += dot4(v, n);
-      const float4 q = mul4(branch_factor(grow, a.w_post, a.beta, i), m);
-      s[1] += dot4(q, add4(dr, scale4(rr, v)));
-      s[2] += dot4(q, n);
-    }
-    block_sum(s, buf[t & 1]);
-    const float cd = rr * s[0] * inv_d;
-    const float ed = a.post_norm ? (s[1] - cd * s[2]) * inv_d : 0.f;
-#pragma unroll 2
-    for (int i = i0; i < a.d; i += step) {
-      float4 n, v, m, dr;
-      load(i, n, v, m, dr);
-      float4 *sp = reinterpret_cast<float4 *>(s_pre + i), *sg = reinterpret_cast<float4 *>(S + i);
-      *sp = add4(*sp, mul4(v, n));
-      if (a.w_pre) v = mul4(v, ld4(a.w_pre + i));
-      const float4 d4 = add4(add4(dr, scale4(rr, v)), scale4(-cd, n));
-      const float4 f = branch_factor(grow, a.w_post, a.beta, i);
-      *sg = add4(*sg, mul4(m, d4));
-      // a row's inputs are read before its outputs are written, element by element: dx may be dx_out, dy y
-      if (a.dx) *reinterpret_cast<float4 *>(a.dx + row + i) = scale4(a.alpha, d4);
-      if (a.dy) st4(a.dy, row + i, a.y_type, scale4(rp, add4(mul4(f, d4), scale4(-ed, m))));
-    }
-  }
-  if (a.y && (a.part_post || a.dgate)) flush();
-  if (a.part_pre)
-    for (int i = i0; i < a.d; i += step)
-      *reinterpret_cast<float4 *>(a.part_pre + (size_t)blockIdx.x * a.d + i) = ld4(s_pre + i);
+      *reinterpret_cast<float4 *>(a.part_pre + (size_t)blk * d + col(c)) = f4(s_pre[c]);
+  if constexpr (CL) row_sync<CL>();  // the other block has written its last sums
 }
 
 // Joins the blocks' column sums in block order, 32 columns a block, in jobs
@@ -574,7 +524,6 @@ __global__ void __launch_bounds__(1024) norm_bwd_wide_kernel(const BwdArgs a) {
 // blocks' rows) has a job of its own, summed by all warps; short ones, at most
 // one per boundary between blocks, are dealt to the warps of kGateJobs jobs.
 constexpr int kGateJobs = 16;
-constexpr int kMaxBwdBlocks = 2048;
 struct JoinArgs {
   const float *part_post, *part_pre, *part_gate;
   float *dw_post, *dw_pre, *dgate;
@@ -582,10 +531,11 @@ struct JoinArgs {
   int long_rows;  // gate rows are long: job 2 + row has row
   int gate_jobs;
 };
-__global__ void __launch_bounds__(256) norm_join_kernel(const JoinArgs a) {
+__global__ void __launch_bounds__(1024) norm_join_kernel(const JoinArgs a) {
   pdl_wait();
   pdl_launch_dependents();
-  __shared__ float buf[8][32];
+  __shared__ float buf[32][32];
+  const int nw = blockDim.x >> 5;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int i = blockIdx.x * 32 + lane;
   const bool in = i < a.d;
@@ -616,20 +566,20 @@ __global__ void __launch_bounds__(256) norm_join_kernel(const JoinArgs a) {
     float s = 0.f;
     if (in) {
 #pragma unroll 8
-      for (int c = b0 + w; c < b1; c += 8)
+      for (int c = b0 + w; c < b1; c += nw)
         s += (c == b0 && job >= 2 ? row_part(c, b0, job - 2) : part + (size_t)c * stride * a.d)[i];
     }
     buf[w][lane] = s;
     __syncthreads();
     if (w == 0 && in) {
-#pragma unroll
-      for (int k = 1; k < 8; ++k) s += buf[k][lane];
+#pragma unroll 7
+      for (int k = 1; k < nw; ++k) s += buf[k][lane];
       put(out + i, s);
     }
     return;
   }
   // the row at boundary b (between blocks b and b + 1), if the boundary is the first inside it
-  for (int b = (job - 2) + a.gate_jobs * w; b < a.G - 1; b += a.gate_jobs * 8) {
+  for (int b = (job - 2) + a.gate_jobs * w; b < a.G - 1; b += a.gate_jobs * nw) {
     const int cut = first_token(a.tokens, a.G, b + 1), row = cut / a.tokens_per_gate;
     if (row * a.tokens_per_gate == cut) continue;
     int b0, b1;

@@ -50,7 +50,8 @@ def _reference(c, x=None, y=None, gate=None, w_post=None, w_pre=None):
 
 
 SHAPES = [(1, 8), (1, 8192), (2, 64), (5, 128), (37, 1000), (300, 136), (130, 2048), (64, 2056), (9, 5120), (7, 7168),
-          (3, 16384), (1000, 24)]
+          (3, 16384), (1000, 24),
+          (5, 8200), (200, 12288), (700, 512), (2100, 72), (150, 6152)]
 KINDS = [(F32, F16, False, 0), (F16, F16, True, 0), (BF16, BF16, True, 1), (F32, F32, True, 7), (BF16, F16, False, 3)]
 
 
