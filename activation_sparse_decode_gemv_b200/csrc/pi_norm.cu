@@ -237,7 +237,8 @@ pi_status pi_block_norm_backward(const pi_block_norm_desc *desc, const float *x_
     }
     const dim3 g(cdiv(d, 32), 2 + j.gate_jobs);
     // more warps where there are few columns and many partial rows
-    PI_CUDA(launch1(NM::norm_join_kernel, g, G > 256 ? 1024 : 256, 0, 0, nullptr, st, j));
+    PI_CUDA(G > 256 ? launch1(NM::norm_join_kernel<32>, g, 1024, 0, 0, nullptr, st, j)
+                    : launch1(NM::norm_join_kernel<8>, g, 256, 0, 0, nullptr, st, j));
   }
   return PI_OK;
 }

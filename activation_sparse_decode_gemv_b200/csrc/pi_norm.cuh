@@ -531,11 +531,11 @@ struct JoinArgs {
   int long_rows;  // gate rows are long: job 2 + row has row
   int gate_jobs;
 };
-__global__ void __launch_bounds__(1024) norm_join_kernel(const JoinArgs a) {
+template <int NW>
+__global__ void __launch_bounds__(NW * 32) norm_join_kernel(const JoinArgs a) {
   pdl_wait();
   pdl_launch_dependents();
-  __shared__ float buf[32][32];
-  const int nw = blockDim.x >> 5;
+  __shared__ float buf[NW][32];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int i = blockIdx.x * 32 + lane;
   const bool in = i < a.d;
@@ -566,20 +566,20 @@ __global__ void __launch_bounds__(1024) norm_join_kernel(const JoinArgs a) {
     float s = 0.f;
     if (in) {
 #pragma unroll 8
-      for (int c = b0 + w; c < b1; c += nw)
+      for (int c = b0 + w; c < b1; c += NW)
         s += (c == b0 && job >= 2 ? row_part(c, b0, job - 2) : part + (size_t)c * stride * a.d)[i];
     }
     buf[w][lane] = s;
     __syncthreads();
     if (w == 0 && in) {
-#pragma unroll 7
-      for (int k = 1; k < nw; ++k) s += buf[k][lane];
+#pragma unroll
+      for (int k = 1; k < NW; ++k) s += buf[k][lane];
       put(out + i, s);
     }
     return;
   }
   // the row at boundary b (between blocks b and b + 1), if the boundary is the first inside it
-  for (int b = (job - 2) + a.gate_jobs * w; b < a.G - 1; b += a.gate_jobs * nw) {
+  for (int b = (job - 2) + a.gate_jobs * w; b < a.G - 1; b += a.gate_jobs * NW) {
     const int cut = first_token(a.tokens, a.G, b + 1), row = cut / a.tokens_per_gate;
     if (row * a.tokens_per_gate == cut) continue;
     int b0, b1;
