@@ -125,7 +125,7 @@ constexpr Tilings kGluTilings{2, {{2, 256}, {2, 128}}, 9000};
 constexpr Tilings kDgluTilings{2, {{1, 256}, {1, 128}}, 10000};
 constexpr Tilings kStoreTilings{4, {{2, 256}, {2, 192}, {1, 256}, {1, 128}}, 6000};
 constexpr Tilings kWeightTilings{2, {{2, 256}, {1, 256}}, 6000};
-constexpr Tilings kI8Tilings{2, {{1, 256}, {1, 128}}, 7000};
+constexpr Tilings kI8Tilings{2, {{1, 256}, {1, 128}}, 7000};  // {2, 256} measured 10% slower (4096 x 5120 x 13824: 245 us, 224)
 
 // Estimated SM cycles of the two kernels.  A tiling's K blocks cost the slower
 // of the MMAs (2 cycles a column and block), the arrival of its bytes at the
@@ -147,7 +147,7 @@ double pair_cost(long long tiles, int pairs, int kb, int mb, int nt, double epil
 // cycle in all, 19 B for one CTA: one token, 5120 x 13824, 108 tiles: 36 us
 // unsplit, 25.5 split by 2, 30.7 by 4, whose clusters take two rounds).
 double split_cost(long long tiles, int ntn, int kb, int nt, int split, int cap) {
-  const int ns = nt <= 16 ? 6 : nt <= 32 ? 5 : nt <= 64 ? 4 : 3;
+  const int ns = GM::split_stages(nt);
   const long long rounds = (tiles + cap - 1) / cap;
   const double active = (double)(tiles < cap ? tiles : cap) * split, stage = 16384.0 + nt * 128.0;
   const double hbm = 16384.0 / ntn / (3450.0 / active < 19.0 ? 3450.0 / active : 19.0);
@@ -172,7 +172,7 @@ Plan choose(int m, int m_rows, int n, int kb, int sms, const Tilings &tilings) {
                                  tilings.epilogue, glu);
       if (cost == 0 || c < cost) cost = c, best = Plan{t.nt, t.mb, 0};
     }
-  for (int nt = 16; nt <= 128; nt *= 2) {
+  for (const int nt : {16, 32, 48, 64, 128}) {
     const long long tiles = (long long)cdiv(m, m_rows) * cdiv(n, nt);
     if (tiles > 65536) continue;
     for (int split = 1; split <= kMaxSplit && (split == 1 || split * 4 <= kb); ++split) {
@@ -219,6 +219,8 @@ cudaError_t run_plan(GM::Args &a, const Plan &p, int dtype, int m_rows, int sms,
     return split_launch<EPI, AMN, 16, T>(a, p.split, st);
   case 32:
     return split_launch<EPI, AMN, 32, T>(a, p.split, st);
+  case 48:
+    return split_launch<EPI, AMN, 48, T>(a, p.split, st);
   case 64:
     return split_launch<EPI, AMN, 64, T>(a, p.split, st);
   default:

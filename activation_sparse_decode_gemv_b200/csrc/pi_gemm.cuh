@@ -812,14 +812,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 // ================================================================ split-K kernel
 constexpr int kSplitThreads = 192;  // producer, MMA issuer, 4 epilogue warps
 
+// ring depth with two CTAs per SM
+__host__ __device__ constexpr int split_stages(int nt) { return nt <= 16 ? 6 : nt <= 48 ? 5 : nt <= 64 ? 4 : 3; }
 template <int NT>
 struct SplitShape {
   static constexpr int ABYTES = 16384;
   static constexpr int STAGE = ABYTES + NT * 128;
-  static constexpr int NS = NT <= 16 ? 6 : NT <= 32 ? 5 : NT <= 64 ? 4 : 3;  // two CTAs per SM
+  static constexpr int NS = split_stages(NT);
   static constexpr int CTRL_OFF = NS * STAGE;
   static constexpr int SMEM = CTRL_OFF + 512 + 1024;
-  static constexpr uint32_t TMEM_COLS = NT < 32 ? 32 : NT;
+  static constexpr uint32_t TMEM_COLS = NT <= 32 ? 32 : NT <= 64 ? 64 : 128;
   static_assert(NT * 512 <= NS * STAGE, "the partial tile fits the ring");
   static_assert(2 * (SMEM + 1024) <= 228 * 1024, "two CTAs per SM");
 };
