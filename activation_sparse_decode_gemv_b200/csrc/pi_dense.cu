@@ -416,6 +416,9 @@ pi_status pi_gated_ffn_forward(pi_gated_ffn_t h, const void *u, int tokens, void
   FfnWs w;
   const pi_status s = ffn_ws(h, tokens, false, ws, ws_bytes, &w);
   if (s != PI_OK) return s;
+  const size_t td = (size_t)tokens * h->d.d_model * 2, tf = (size_t)tokens * h->d.d_ffn * 2;
+  const Range r[] = {{y, td}, {gate, tf}, {up, tf}, {ws, ffn_ws_bytes(h, tokens, false)}, {u, td}};
+  if (overlapping(r, 4, 5)) return PI_ERR_INVALID_ARG;
   if (!h->maps_ok) return PI_ERR_CUDA;
   cudaStream_t st = (cudaStream_t)stream;
   return h->d.dtype == PI_DT_F16 ? ffn_forward<__half>(h, u, tokens, y, gate, up, w, st)
@@ -446,6 +449,11 @@ pi_status pi_gated_ffn_backward(pi_gated_ffn_t h, const void *u, const void *gat
   FfnWs w;
   const pi_status s = ffn_ws(h, tokens, true, ws, ws_bytes, &w);
   if (s != PI_OK) return s;
+  const size_t td = (size_t)tokens * h->d.d_model * 2, tf = (size_t)tokens * h->d.d_ffn * 2;
+  const size_t fd = (size_t)h->d.d_ffn * h->d.d_model * type_size(grad_dtype);
+  const Range r[] = {{du, td}, {dw_gate, fd}, {dw_up, fd}, {dw_down_t, fd}, {ws, ffn_ws_bytes(h, tokens, true)},
+                     {u, td},  {gate, tf},    {up, tf},    {dy, td}};
+  if (overlapping(r, 5, 9)) return PI_ERR_INVALID_ARG;
   if (!h->maps_ok) return PI_ERR_CUDA;
   return h->d.dtype == PI_DT_F16
              ? ffn_backward<__half>(h, u, gate, up, dy, tokens, du, dw_gate, dw_up, dw_down_t, grad_dtype, acc, w, st)
@@ -474,6 +482,10 @@ pi_status pi_matmul_i8(const int8_t *xq, const float *x_scales, const int8_t *wq
   if (!ws) return PI_ERR_WORKSPACE;
   if (!aligned16(ws)) return PI_ERR_MISALIGNED;
   if (ws_bytes < kHeader) return PI_ERR_WORKSPACE;
+  const size_t t4 = (size_t)tokens * 4, n4 = (size_t)n * 4;
+  const Range r[] = {{y, (size_t)tokens * n * type_size(y_dtype)}, {ws, kHeader}, {xq, (size_t)tokens * k},
+                     {x_scales, t4}, {wq, (size_t)n * k}, {w_scales, n4}, {bias, n4}};
+  if (overlapping(r, 2, 7)) return PI_ERR_INVALID_ARG;
   const int sms = device_sm_count();
   if (sms <= 0) return PI_ERR_CUDA;
   GM::Args a{};

@@ -95,6 +95,18 @@ inline bool overlap(const void *p, size_t pn, const void *q, size_t qn) {
   const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
   return p && q && a < b + qn && b < a + pn;
 }
+// Memory of an argument (null: none).
+struct Range {
+  const void *p;
+  size_t n;
+};
+// whether one of the first n_out ranges (outputs) shares memory with another of the n
+inline bool overlapping(const Range *r, int n_out, int n) {
+  for (int i = 0; i < n_out; ++i)
+    for (int j = i + 1; j < n; ++j)
+      if (overlap(r[i].p, r[i].n, r[j].p, r[j].n)) return true;
+  return false;
+}
 inline bool is_half(int t) { return t == PI_DT_F16 || t == PI_DT_BF16; }
 inline bool is_type(int t) { return t == PI_DT_F32 || is_half(t); }
 inline size_t type_size(int t) { return t == PI_DT_F32 ? 4 : 2; }

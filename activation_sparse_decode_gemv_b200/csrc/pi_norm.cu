@@ -153,7 +153,8 @@ pi_status pi_block_norm_forward(const pi_block_norm_desc *desc, const float *x, 
   a.x = x, a.y = y;
   a.w_post = desc->w_post, a.w_pre = desc->w_pre, a.gate = desc->gate;
   a.x_out = x_out, a.u = u, a.rstd_post = rstd_post, a.rstd_pre = rstd_pre;
-  a.tokens = tokens, a.d = desc->d_model, a.tokens_per_gate = desc->tokens_per_gate;
+  a.tokens = tokens, a.d = desc->d_model;
+  a.tokens_per_gate = desc->tokens_per_gate < tokens ? desc->tokens_per_gate : tokens;
   a.y_type = desc->y_dtype, a.u_type = desc->u_dtype, a.post_norm = desc->post_norm ? 1 : 0;
   a.eps = desc->eps, a.alpha = desc->residual_scale, a.beta = desc->branch_scale;
   const int sms = device_sm_count();
@@ -219,7 +220,8 @@ pi_status pi_block_norm_backward(const pi_block_norm_desc *desc, const float *x_
   a.part_post = dw_post ? part : nullptr;
   a.part_pre = dw_pre ? part + (size_t)G * d : nullptr;
   a.part_gate = part + (size_t)2 * G * d;
-  a.tokens = tokens, a.d = d, a.tokens_per_gate = desc->tokens_per_gate;
+  a.tokens = tokens, a.d = d;
+  a.tokens_per_gate = desc->tokens_per_gate < tokens ? desc->tokens_per_gate : tokens;
   a.y_type = desc->y_dtype, a.u_type = desc->u_dtype, a.post_norm = desc->post_norm ? 1 : 0;
   a.accumulate = acc;
   a.alpha = desc->residual_scale, a.beta = desc->branch_scale;
@@ -229,10 +231,10 @@ pi_status pi_block_norm_backward(const pi_block_norm_desc *desc, const float *x_
     NM::JoinArgs j{};
     j.part_post = a.part_post, j.part_pre = a.part_pre, j.part_gate = a.part_gate;
     j.dw_post = dw_post, j.dw_pre = dw_pre, j.dgate = dgate;
-    j.G = G, j.tokens = tokens, j.d = d, j.tokens_per_gate = desc->tokens_per_gate, j.accumulate = acc;
+    j.G = G, j.tokens = tokens, j.d = d, j.tokens_per_gate = a.tokens_per_gate, j.accumulate = acc;
     if (dgate) {
-      const int rows = cdiv(tokens, desc->tokens_per_gate);
-      j.long_rows = (long long)desc->tokens_per_gate * G > 8ll * tokens;  // fewer than G / 8 rows
+      const int rows = cdiv(tokens, a.tokens_per_gate);
+      j.long_rows = (long long)a.tokens_per_gate * G > 8ll * tokens;  // fewer than G / 8 rows
       j.gate_jobs = j.long_rows ? rows : rows < NM::kGateJobs ? rows : NM::kGateJobs;
     }
     const dim3 g(cdiv(d, 32), 2 + j.gate_jobs);
@@ -250,6 +252,8 @@ pi_status pi_quantize_i8(const void *x, int x_dtype, int rows, int k, int8_t *q,
   if (rows == 0) return PI_OK;
   if (!x || !q || !scales) return PI_ERR_INVALID_ARG;
   if (!aligned16(x) || !aligned16(q) || !aligned16(scales)) return PI_ERR_MISALIGNED;
+  const Range r[] = {{q, (size_t)rows * k}, {scales, (size_t)rows * 4}, {x, (size_t)rows * k * type_size(x_dtype)}};
+  if (overlapping(r, 2, 3)) return PI_ERR_INVALID_ARG;
   const int sms = device_sm_count();
   if (sms <= 0) return PI_ERR_CUDA;
   // a thread keeps up to 4 chunks of 8 elements; more threads for longer rows and for few rows

@@ -70,6 +70,11 @@ def test_gated_ffn_calls(lib):
     assert fwd(h, A, 1, B_, None, None, C_, 256 + 255, None) == WS
     assert fwd(h, A, 1, B_, None, None, vp(0x1008), 1 << 20, None) == ALIGN
     assert fwd(h, None, 0, None, None, None, None, 0, None) == OK  # no tokens: nothing is read
+    # outputs over inputs, each other or the workspace
+    assert fwd(h, A, 1, A, None, None, C_, 1 << 20, None) == ARG
+    assert fwd(h, A, 2, B_, vp(B_.value + 128), None, C_, 1 << 20, None) == ARG
+    assert fwd(h, A, 1, B_, D_, D_, C_, 1 << 20, None) == ARG
+    assert fwd(h, A, 1, B_, C_, None, C_, 1 << 20, None) == ARG
     bwd = lib.pi_gated_ffn_backward
     ok = [h, A, B_, C_, D_, 4, E_, F_, G_, H_, pb.PI_DT_F32, 0, vp(0x9000), 1 << 20, None]
 
@@ -80,6 +85,8 @@ def test_gated_ffn_calls(lib):
         return bwd(*a)
     assert b(_0=None) == ARG and b(_1=None) == ARG and b(_2=None) == ARG and b(_3=None) == ARG and b(_4=None) == ARG
     assert b(_5=-1) == UNSUP and b(_10=7) == ARG and b(_10=pb.PI_DT_BF16) == UNSUP and b(_11=2) == ARG
+    assert b(_6=D_) == ARG and b(_6=A) == ARG and b(_8=F_) == ARG and b(_9=vp(E_.value + 64)) == ARG
+    assert b(_7=vp(0x9100)) == ARG  # over the workspace
     assert b(_7=vp(0x18)) == ALIGN and b(_12=None) == WS and b(_13=256 + 3 * 1024 - 1) == WS
     lib.pi_gated_ffn_destroy(h)
 
@@ -137,6 +144,7 @@ def test_matmul_i8_calls(lib):
     assert qz(A, 3, 4, 64, B_, C_, None) == ARG and qz(A, 0, 4, 0, B_, C_, None) == ARG
     assert qz(A, 0, 4, 40, B_, C_, None) == UNSUP and qz(A, 0, -1, 64, B_, C_, None) == UNSUP
     assert qz(A, 0, 1, 131072, B_, C_, None) == UNSUP and qz(vp(8), 0, 4, 64, B_, C_, None) == ALIGN
+    assert qz(A, 0, 4, 64, A, C_, None) == ARG and qz(A, 0, 4, 64, B_, vp(B_.value + 16), None) == ARG
     assert qz(None, 0, 0, 64, None, None, None) == OK
     n = C.c_size_t()
     assert lib.pi_matmul_i8_workspace_size(4, 100, 64, C.byref(n)) == OK and n.value >= 256
@@ -154,6 +162,7 @@ def test_matmul_i8_calls(lib):
         assert mm(**{f"_{i}": None}) == ARG
         assert mm(**{f"_{i}": vp(0x18)}) == ALIGN
     assert mm(_5=-1) == UNSUP and mm(_6=0) == ARG and mm(_7=72) == UNSUP and mm(_7=131072) == UNSUP
+    assert mm(_8=A) == ARG and mm(_8=C_) == ARG and mm(_4=E_) == ARG and mm(_10=E_) == ARG
     assert mm(_9=5) == ARG and mm(_10=None) == WS and mm(_11=255) == WS and mm(_10=vp(0x18)) == ALIGN
     assert mm(_0=None, _1=None, _5=0, _8=None, _10=None) == OK
 

@@ -325,3 +325,42 @@ def test_offsets_past_32_bits(cuda_device):
     pb.pi_block_norm_backward(n, x5, None, None, kr5, du[-5:].clone(), None, dx5, None, ws, dw_pre=dw5)
     assert torch.equal(dx[-5:], dx5) and torch.all(dx[:-5] == 0)
     assert torch.all((dw - dw5).abs() <= 16 * E * (x5 * kr5[:, None]).abs().sum(0) * 0.25)
+
+
+def test_gate_rows_longer_than_the_batch(cuda_device):
+    """tokens_per_gate up to the largest int: one row for all tokens."""
+    T, d = 90, 264
+    c = _case(T, d, F16, F16, True, T, seed=12)
+    big = pb.BlockNorm(d, y_dtype=F16, u_dtype=F16, eps=EPS, residual_scale=c["alpha"], branch_scale=c["beta"],
+                       post_norm=True, w_post=c["w_post"], w_pre=c["w_pre"], gate=c["gate"],
+                       tokens_per_gate=2 ** 31 - 1)
+    outs = []
+    for norm in (c["norm"], big):
+        r, u = torch.empty(T, d, device="cuda"), torch.empty(T, d, dtype=F16, device="cuda")
+        kp, kr = torch.empty(T, device="cuda"), torch.empty(T, device="cuda")
+        pb.pi_block_norm_forward(norm, c["x"], c["y"], r, u, kp, kr)
+        out = _run_backward(dict(c, norm=norm), T, d, kp, kr, r)
+        outs.append([r, u, *out.values()])
+    assert all(torch.equal(a, b) for a, b in zip(*outs))
+
+
+def test_two_streams_at_once(cuda_device):
+    """Calls on two streams with a workspace each do not disturb one another."""
+    T, d = 300, 2056
+    cs = [_case(T, d, BF16, BF16, True, 64, seed=s) for s in (20, 21)]
+    fwd = []
+    for c in cs:
+        r, u = torch.empty(T, d, device="cuda"), torch.empty(T, d, dtype=BF16, device="cuda")
+        kp, kr = torch.empty(T, device="cuda"), torch.empty(T, device="cuda")
+        pb.pi_block_norm_forward(c["norm"], c["x"], c["y"], r, u, kp, kr)
+        fwd.append((kp, kr, r))
+    want = [_run_backward(c, T, d, *f) for c, f in zip(cs, fwd)]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in cs], [None, None]
+    for _ in range(5):
+        for k, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                got[k] = _run_backward(cs[k], T, d, *fwd[k])
+    torch.cuda.synchronize()
+    for a, b in zip(want, got):
+        assert all(torch.equal(a[x], b[x]) for x in a if a[x] is not None)

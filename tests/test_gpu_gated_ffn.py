@@ -304,3 +304,93 @@ def test_offsets_past_32_bits(cuda_device):
         assert torch.equal(y[rows], yr.to(dtype))
         *_, dg, dp, _ = ref.ffn_backward("relu", u6, gr, pr, dy6, wg.to(D), wu.to(D), wd.to(D))
         assert torch.equal(du[rows], (dg @ wg.to(D) + dp @ wu.to(D)).to(dtype))
+
+
+CAPTURE_FIRST = """
+import torch
+from activation_sparse_decode_gemv_b200 import binding as pb
+T, d, f = %d, 264, 1032
+g = torch.Generator(device="cuda").manual_seed(0)
+w = [(torch.randn(f, d, generator=g, device="cuda") * 0.05).half() for _ in range(3)]
+layer = pb.GatedFfnLayer(*w)
+ws = pb.make_gated_ffn_workspace(layer, T, True)
+u = torch.randn(T, d, generator=g, device="cuda").half()
+y, gp, up = torch.empty_like(u), u.new_empty(T, f), u.new_empty(T, f)
+du, dw = torch.empty_like(u), [torch.empty_like(w[0]) for _ in range(3)]
+n = pb.BlockNorm(d, y_dtype=torch.float16, u_dtype=torch.float16, post_norm=True)
+x, r, kp, kr = torch.randn(T, d, generator=g, device="cuda"), u.new_empty(T, d).float(), u.new_empty(T).float(), u.new_empty(T).float()
+nws, dx, dwp = pb.make_block_norm_workspace(n, T), torch.empty(T, d, device="cuda"), torch.empty(d, device="cuda")
+q, s, wq, wsc = u.new_empty(T, 256).to(torch.int8), kp.clone(), torch.ones(96, 256, dtype=torch.int8, device="cuda"), torch.ones(96, device="cuda")
+z, xi = torch.empty(T, 96, device="cuda"), torch.randn(T, 256, generator=g, device="cuda")
+iws = pb.make_matmul_i8_workspace(T, 96, 256)
+torch.cuda.synchronize()
+def step():
+    pb.pi_gated_ffn_forward(layer, u, y, ws, gate=gp, up=up)
+    pb.pi_block_norm_forward(n, x, y, r, None, rstd_post=kp)
+    pb.pi_block_norm_backward(n, None, y, kp, None, None, x, dx, None, nws, dw_post=dwp)
+    pb.pi_gated_ffn_backward(layer, u, gp, up, y, ws, du, *dw)
+    pb.pi_quantize_i8(xi, q, s)
+    pb.pi_matmul_i8(q, s, wq, wsc, z, iws)
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    step()
+graph.replay()
+torch.cuda.synchronize()
+got = [t.clone() for t in (y, r, dx, dwp, du, *dw, z)]
+step()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, (y, r, dx, dwp, du, *dw, z)))
+assert pb.pi_get_device_status(ws) == 0 and pb.pi_get_device_status(iws) == 0
+print("captured first")
+"""
+
+
+@pytest.mark.parametrize("T", [3, 400])
+def test_first_calls_of_a_process_may_be_captured(cuda_device, T):
+    """Nothing that a first call sets up needs a call outside of a capture."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    out = subprocess.run([sys.executable, "-c", CAPTURE_FIRST % T], cwd=root, capture_output=True, text=True, timeout=300)
+    assert out.returncode == 0 and "captured first" in out.stdout, out.stderr[-2000:]
+
+
+def test_one_of_the_kept_outputs_alone(cuda_device):
+    for T in (5, 300):
+        u, wg, wu, wd, _ = _rand_case(T, 264, 520, torch.float16, 41)
+        layer, ws = _layer(wg, wu, wd, "silu", T)
+        y, g, p = _forward(layer, u, ws)
+        for k, want in (("gate", g), ("up", p)):
+            y2, out = torch.empty_like(y), torch.empty_like(want)
+            pb.pi_gated_ffn_forward(layer, u, y2, ws, **{k: out})
+            assert torch.equal(out, want) and torch.equal(y, y2)
+
+
+def test_two_streams_at_once(cuda_device):
+    """Calls on two streams with a workspace each, large and small, forward and backward."""
+    jobs = []
+    for k, (T, d, f) in enumerate([(300, 1032, 2056), (2, 2056, 4104)]):
+        u, wg, wu, wd, dy = _rand_case(T, d, f, torch.bfloat16, 50 + k)
+        layer, ws = _layer(wg, wu, wd, "silu", T, True)
+        o = [torch.empty(T, n, dtype=torch.bfloat16, device="cuda") for n in (d, f, f, d)]
+        dw = [torch.empty_like(wg) for _ in range(3)]
+
+        def job(layer=layer, ws=ws, u=u, dy=dy, o=o, dw=dw):
+            pb.pi_gated_ffn_forward(layer, u, o[0], ws, gate=o[1], up=o[2])
+            pb.pi_gated_ffn_backward(layer, u, o[1], o[2], dy, ws, o[3], *dw)
+        job()
+        jobs.append((job, o + dw, [t.clone() for t in o + dw]))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in jobs]
+    for _, outs, _ in jobs:
+        for t in outs:
+            t.zero_()
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for (job, _, _), st in zip(jobs, streams):
+            with torch.cuda.stream(st):
+                job()
+    torch.cuda.synchronize()
+    for _, outs, want in jobs:
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))
