@@ -175,7 +175,7 @@ Plan choose(int m, int m_rows, int n, int kb, int sms, const Tilings &tilings) {
   for (const int nt : {16, 32, 48, 64, 128}) {
     const long long tiles = (long long)cdiv(m, m_rows) * cdiv(n, nt);
     if (tiles > 65536) continue;
-    for (int split = 1; split <= kMaxSplit && (split == 1 || split * 4 <= kb); ++split) {
+    for (int split = 1; split <= kMaxSplit && (split == 1 || split * 2 <= kb); ++split) {
       const int cap = caps->n[split];
       // clusters of 3 and 7 leave SMs with one CTA where others have two: 333 tokens, 1032 x 2760 (66
       // tiles) 15.5 us split by 3, 13.2 by 4; 40 tiles of K 13824 83.8 us by 7, 70.5 by 6

@@ -845,6 +845,20 @@ __global__ void __launch_bounds__(kSplitThreads, 2) split_gemm_kernel(const __gr
   const int row0 = mtile * MROWS, col0 = ntile * NT;
   const int k0 = (int)((long long)a.kb * rank / split), k1 = (int)((long long)a.kb * (rank + 1) / split);
 
+  volatile int *abort_flag = &C.abort_flag;
+  auto start_a = [&](int kb, int st) {
+    int map, blk;
+    k_at(a, 0, kb, map, blk);
+    mbar_expect_tx(&C.full[st], S::STAGE);
+    load_a<EPI, AMN>(a, map, blk, row0, su32(smem + st * S::STAGE),
+                     [&](uint32_t d, const CUtensorMap *tm, int x, int y) { tma_load_2d(d, tm, x, y, &C.full[st]); });
+  };
+  auto start_b = [&](int kb, int st) {
+    int map, blk;
+    k_at(a, 0, kb, map, blk);
+    tma_load_2d(su32(smem + st * S::STAGE + S::ABYTES), &a.mb[map], blk * (I8 ? 128 : 64), col0, &C.full[st]);
+  };
+  const int first = min(S::NS, k1 - k0);  // K blocks that fill the ring
   if (tid == 0) {
     for (int s = 0; s < S::NS; ++s) {
       mbar_init(&C.full[s], 1);
@@ -853,38 +867,35 @@ __global__ void __launch_bounds__(kSplitThreads, 2) split_gemm_kernel(const __gr
     mbar_init(&C.accfull[0], 1);
     C.abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    proxy_fence_async();
+    // The producer is this thread: it fills the ring while the others set up.
+    // Weights that the previous kernel of the same call does not write are
+    // loaded before that one ends.
+    if (a.early_a)
+      for (int i = 0; i < first; ++i) start_a(k0 + i, i);
+    pdl_wait();
+    pdl_launch_dependents();  // after the wait: the next kernel may rely on everything before this one
+    for (int i = 0; i < first; ++i) {
+      if (!a.early_a) start_a(k0 + i, i);
+      start_b(k0 + i, i);
+    }
   }
   if (warp == 1) tmem_alloc(&C.tmem, S::TMEM_COLS);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = C.tmem;
-  volatile int *abort_flag = &C.abort_flag;
   bool fine = true;
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer (one lane)
     if (lane == 0) {
-      auto start_a = [&](int kb, int s) {
-        int map, blk;
-        k_at(a, 0, kb, map, blk);
-        mbar_expect_tx(&C.full[s], S::STAGE);
-        load_a<EPI, AMN>(a, map, blk, row0, su32(smem + s * S::STAGE),
-                         [&](uint32_t d, const CUtensorMap *tm, int x, int y) { tma_load_2d(d, tm, x, y, &C.full[s]); });
-      };
-      // the first stages' weights do not depend on the previous kernel of the same call
-      const int early = a.early_a ? min(S::NS, k1 - k0) : 0;
-      for (int i = 0; i < early; ++i) start_a(k0 + i, i);
-      pdl_wait();
-      pdl_launch_dependents();  // after the wait: the next kernel may rely on everything before this one
-      for (int kb = k0; kb < k1; ++kb) {
+      for (int kb = k0 + first; kb < k1; ++kb) {
         const int i = kb - k0, s = i % S::NS;
         const unsigned ph = (unsigned)((i / S::NS) & 1);
-        if (i >= S::NS && !mbar_wait(&C.empty[s], ph ^ 1u, abort_flag, a.status)) break;
-        if (i >= early) start_a(kb, s);
-        int map, blk;
-        k_at(a, 0, kb, map, blk);
-        tma_load_2d(su32(smem + s * S::STAGE + S::ABYTES), &a.mb[map], blk * (I8 ? 128 : 64), col0, &C.full[s]);
+        if (!mbar_wait(&C.empty[s], ph ^ 1u, abort_flag, a.status)) break;
+        start_a(kb, s);
+        start_b(kb, s);
       }
     }
     __syncwarp();
@@ -962,7 +973,16 @@ __global__ void __launch_bounds__(kSplitThreads, 2) split_gemm_kernel(const __gr
         }
       }
     };
-    auto finish = [&](int e, float (&v)[4], float (&w)[4]) {
+    // E_DGLU: g and p of an item (rows of a multiple of 8 features)
+    auto load_gp = [&](int e, uint4 &gp) {
+      const int n = col0 + e / Q, m = row0 + (e % Q) * 4;
+      if (m >= a.m) return;
+      const size_t at = (size_t)n * a.ldo + m;
+      const uint2 g = *reinterpret_cast<const uint2 *>(reinterpret_cast<const T *>(a.gate_in) + at);
+      const uint2 p = *reinterpret_cast<const uint2 *>(reinterpret_cast<const T *>(a.up_in) + at);
+      gp = make_uint4(g.x, g.y, p.x, p.y);
+    };
+    auto finish = [&](int e, float (&v)[4], float (&w)[4], const uint4 &gp) {
       const int n = col0 + e / Q, m = row0 + (e % Q) * 4;
       if (m >= a.m) return;
       if constexpr (EPI == E_GLU) {
@@ -982,14 +1002,11 @@ __global__ void __launch_bounds__(kSplitThreads, 2) split_gemm_kernel(const __gr
         else if (a.out_type == O_F16) put_row4<__half>(a, a.out[0], m, n, v);
         else put_row4<__nv_bfloat16>(a, a.out[0], m, n, v);
       } else if constexpr (EPI == E_DGLU) {
-        const size_t at = (size_t)n * a.ldo + m;  // rows of a multiple of 8 features
-        const uint2 gw = *reinterpret_cast<const uint2 *>(reinterpret_cast<const T *>(a.gate_in) + at);
-        const uint2 pw = *reinterpret_cast<const uint2 *>(reinterpret_cast<const T *>(a.up_in) + at);
         float g[4], p[4], dg[4], dp[4], av[4];
-        unpack2<T>(gw.x, g[0], g[1]);
-        unpack2<T>(gw.y, g[2], g[3]);
-        unpack2<T>(pw.x, p[0], p[1]);
-        unpack2<T>(pw.y, p[2], p[3]);
+        unpack2<T>(gp.x, g[0], g[1]);
+        unpack2<T>(gp.y, g[2], g[3]);
+        unpack2<T>(gp.z, p[0], p[1]);
+        unpack2<T>(gp.w, p[2], p[3]);
         dglu<4>(a.act, v, g, p, dg, dp, av);
         put_row4<T>(a, a.gate_out, m, n, dg);
         put_row4<T>(a, a.up_out, m, n, dp);
@@ -1001,11 +1018,16 @@ __global__ void __launch_bounds__(kSplitThreads, 2) split_gemm_kernel(const __gr
     };
     for (int e = e0 + tid; e < e1; e += 2 * kSplitThreads) {
       float v0[4], w0[4], v1[4], w1[4];
+      uint4 g0, g1;
       const bool two = e + kSplitThreads < e1;
+      if constexpr (EPI == E_DGLU) {
+        load_gp(e, g0);
+        if (two) load_gp(e + kSplitThreads, g1);
+      }
       sum(e, v0, w0);
       if (two) sum(e + kSplitThreads, v1, w1);
-      finish(e, v0, w0);
-      if (two) finish(e + kSplitThreads, v1, w1);
+      finish(e, v0, w0, g0);
+      if (two) finish(e + kSplitThreads, v1, w1, g1);
     }
   }
   tc_fence_before();

@@ -238,7 +238,7 @@ pi_status pi_block_norm_backward(const pi_block_norm_desc *desc, const float *x_
       j.gate_jobs = j.long_rows ? rows : rows < NM::kGateJobs ? rows : NM::kGateJobs;
     }
     const dim3 g(cdiv(d, 32), 2 + j.gate_jobs);
-    // more warps where there are few columns and many partial rows
+    // many partial rows: more warps, so that their loads go out together
     PI_CUDA(G > 256 ? launch1(NM::norm_join_kernel<32>, g, 1024, 0, 0, nullptr, st, j)
                     : launch1(NM::norm_join_kernel<8>, g, 256, 0, 0, nullptr, st, j));
   }
