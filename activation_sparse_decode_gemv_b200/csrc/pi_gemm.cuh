@@ -16,12 +16,23 @@
 // Elements outside a matrix read as zero, so ragged edges add exact zeros.
 //
 // Two kernels:
-//   pair_gemm_kernel   many tiles: CTA pairs (cta_group::2), 256 x NT tiles,
-//                      persistent, accumulators double-buffered so that the
-//                      epilogue of a tile runs under the next tile's MMAs;
+//   pair_gemm_kernel   many tiles: CTA pairs (cta_group::2), tiles of one or
+//                      two 256-row blocks x NT columns, persistent; the
+//                      epilogue of a tile runs under the next tile's MMAs
+//                      (two accumulator buffers), or half of it does (one).
+//                      In isolation the tensor pipe is 85% active (gate | up
+//                      product of 4096 x 5120 x 13824, 16 bits); back to back
+//                      the 1000 W power cap bounds it: 1.31 PFLOP/s for 2048 x
+//                      8192 x 28672 against 1.28 for three library products,
+//                      where the L2 traffic of a block that each B tile
+//                      serves twice counts for energy as much as for time.
 //   split_gemm_kernel  few tokens: 128 x NT tiles, K split over a cluster's
 //                      CTAs, partial sums joined through distributed shared
 //                      memory in rank order (no workspace, no atomics).
+//                      Bound by HBM: 5.9 TB/s of weights at one token, 5.2 at
+//                      45 (5120 x 13824, 4096 x 16384); a small product is
+//                      about 6 us, of which 0.7 set-up, 0.7 first load, 1 each
+//                      cluster barrier, 1 to 3 the join.
 // Every mbarrier wait is bounded; a wait that gives up records
 // PI_ERR_TIMEOUT and the kernel ends.
 #pragma once
@@ -486,8 +497,10 @@ constexpr int kLead = 2;           // one buffer of two blocks: K blocks that bl
 // A pair's tile is MB accumulator blocks of 256 rows (128 per CTA) x NT
 // columns: MB x 256 features, or for E_GLU (MB = 2) the gate rows and the up
 // rows of the same 256 neurons, so that a lane holds both of a neuron.  Two
-// blocks halve the B reads per product.  Tensor memory holds BUFS tiles: the
-// accumulators of two tiles alternate where they fit.
+// blocks halve the B reads per product: 48 KB a K block instead of 64 for the
+// same MMAs (weight gradients of 4096 x 5120 x 13824 1313 us against 1399 to
+// 1488).  Tensor memory holds BUFS tiles: the accumulators of two tiles
+// alternate where they fit.
 template <int EPI, int MB, int NT>
 struct PairShape {
   static constexpr int NB = NT / 2;            // B rows that one CTA of the pair loads
