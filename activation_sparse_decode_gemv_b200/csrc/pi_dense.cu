@@ -118,14 +118,17 @@ struct Tilings {
   int n;
   struct {
     int mb, nt;
-  } t[4];
+  } t[8];
   double epilogue;
 };
-constexpr Tilings kGluTilings{2, {{2, 256}, {2, 128}}, 9000};
-constexpr Tilings kDgluTilings{2, {{1, 256}, {1, 128}}, 10000};
-constexpr Tilings kStoreTilings{4, {{2, 256}, {2, 192}, {1, 256}, {1, 128}}, 6000};
+// 160 to 224 columns waste fewer of the last tile's where tokens are not a multiple of 256
+constexpr Tilings kGluTilings{5, {{2, 256}, {2, 224}, {2, 192}, {2, 160}, {2, 128}}, 9000};
+constexpr Tilings kDgluTilings{5, {{1, 256}, {1, 224}, {1, 192}, {1, 160}, {1, 128}}, 10000};
+constexpr Tilings kStoreTilings{
+    8, {{2, 256}, {2, 224}, {2, 192}, {2, 160}, {1, 256}, {1, 192}, {1, 160}, {1, 128}}, 6000};
 constexpr Tilings kWeightTilings{2, {{2, 256}, {1, 256}}, 6000};
-constexpr Tilings kI8Tilings{2, {{1, 256}, {1, 128}}, 7000};  // {2, 256} measured 10% slower (4096 x 5120 x 13824: 245 us, 224)
+// {2, 256} measured 10% slower (4096 x 5120 x 13824: 245 us, 224)
+constexpr Tilings kI8Tilings{5, {{1, 256}, {1, 224}, {1, 192}, {1, 160}, {1, 128}}, 7000};
 
 // Estimated SM cycles of the two kernels.  A tiling's K blocks cost the slower
 // of the MMAs (2 cycles a column and block), the arrival of its bytes at the
@@ -194,6 +197,23 @@ uint32_t idesc(int dtype, bool i8, int M, int N, int a_mn, int b_mn) {
          (uint32_t)(N >> 3) << 17 | (uint32_t)(M >> 4) << 24;
 }
 
+// the tilings of the tables above
+template <int EPI, int AMN, int MB, typename T>
+cudaError_t pair_dispatch(const GM::Args &a, int nt, int sms, cudaStream_t st) {
+  if constexpr (EPI == GM::E_GLU || !(EPI == GM::E_STORE && MB == 2))
+    if (nt == 128) return pair_launch<EPI, AMN, 0, MB, 128, T>(a, sms, st);
+  if constexpr (!(EPI == GM::E_STORE && MB == 1))
+    if (nt == 224) return pair_launch<EPI, AMN, 0, MB, 224, T>(a, sms, st);
+  switch (nt) {
+  case 160:
+    return pair_launch<EPI, AMN, 0, MB, 160, T>(a, sms, st);
+  case 192:
+    return pair_launch<EPI, AMN, 0, MB, 192, T>(a, sms, st);
+  default:
+    return pair_launch<EPI, AMN, 0, MB, 256, T>(a, sms, st);
+  }
+}
+
 template <int EPI, int AMN, typename T>
 cudaError_t run_plan(GM::Args &a, const Plan &p, int dtype, int m_rows, int sms, cudaStream_t st) {
   if (!p.nt) return cudaErrorUnknown;
@@ -201,18 +221,10 @@ cudaError_t run_plan(GM::Args &a, const Plan &p, int dtype, int m_rows, int sms,
   a.nt = cdiv(a.n, p.nt);
   a.idesc = idesc(dtype, EPI == GM::E_I8, p.split ? 128 : 256, p.nt, AMN, 0);
   if (!p.split) {
-    if constexpr (EPI == GM::E_GLU) {
-      return p.nt == 256 ? pair_launch<EPI, AMN, 0, 2, 256, T>(a, sms, st)
-                         : pair_launch<EPI, AMN, 0, 2, 128, T>(a, sms, st);
-    } else {
-      if constexpr (EPI == GM::E_STORE) {
-        if (p.mb == 2)
-          return p.nt == 256 ? pair_launch<EPI, AMN, 0, 2, 256, T>(a, sms, st)
-                             : pair_launch<EPI, AMN, 0, 2, 192, T>(a, sms, st);
-      }
-      return p.nt == 256 ? pair_launch<EPI, AMN, 0, 1, 256, T>(a, sms, st)
-                         : pair_launch<EPI, AMN, 0, 1, 128, T>(a, sms, st);
-    }
+    if constexpr (EPI == GM::E_GLU) return pair_dispatch<EPI, AMN, 2, T>(a, p.nt, sms, st);
+    if constexpr (EPI == GM::E_STORE)
+      if (p.mb == 2) return pair_dispatch<EPI, AMN, 2, T>(a, p.nt, sms, st);
+    if constexpr (EPI != GM::E_GLU) return pair_dispatch<EPI, AMN, 1, T>(a, p.nt, sms, st);
   }
   switch (p.nt) {
   case 16:

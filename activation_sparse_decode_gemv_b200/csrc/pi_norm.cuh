@@ -49,7 +49,6 @@ PI_DEV void st4(void *p, size_t i, int type, float4 v) {
 PI_DEV float4 mul4(float4 a, float4 b) { return make_float4(a.x * b.x, a.y * b.y, a.z * b.z, a.w * b.w); }
 PI_DEV float4 scale4(float s, float4 a) { return make_float4(s * a.x, s * a.y, s * a.z, s * a.w); }
 PI_DEV float4 add4(float4 a, float4 b) { return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w); }
-PI_DEV float dot4(float4 a, float4 b) { return fmaf(a.w, b.w, fmaf(a.z, b.z, fmaf(a.y, b.y, a.x * b.x))); }
 PI_DEV float4 one4() { return make_float4(1.f, 1.f, 1.f, 1.f); }
 PI_DEV float4 zero4() { return make_float4(0.f, 0.f, 0.f, 0.f); }
 

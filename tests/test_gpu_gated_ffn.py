@@ -19,7 +19,8 @@ TYPES = [torch.float16, torch.bfloat16]
 SHAPES = [(1, 8, 8), (1, 520, 264), (2, 64, 128), (3, 72, 40), (16, 256, 512), (17, 264, 136), (32, 1000, 64),
           (33, 136, 1032), (64, 512, 384), (65, 776, 2056), (128, 128, 128), (129, 1032, 520), (200, 2056, 4104),
           (256, 512, 512), (300, 2568, 8), (513, 264, 2760), (1025, 72, 5128),
-          (1500, 4104, 1032), (2000, 4104, 2056), (300, 520, 5128), (700, 2056, 4104)]
+          (1500, 4104, 1032), (2000, 4104, 2056), (300, 520, 5128), (700, 2056, 4104),
+          (430, 1544, 5128), (440, 5128, 2056), (380, 4104, 4104), (310, 2568, 5640), (620, 2056, 4616)]
 
 
 def _ints(gen, *shape, lo, hi, dtype, keep=1.0):

@@ -14,7 +14,8 @@ E = 2.0 ** -24
 F32, F16, BF16 = torch.float32, torch.float16, torch.bfloat16
 SHAPES = [(1, 1, 16), (1, 1000, 528), (2, 129, 4096), (16, 128, 128), (17, 333, 272), (33, 1031, 1040), (64, 256, 2048),
           (65, 77, 144), (128, 512, 384), (129, 513, 1024), (200, 4099, 640), (257, 2050, 1296), (700, 1111, 400),
-          (1500, 4099, 1040), (1000, 9001, 1040), (1600, 4099, 384), (2000, 5000, 400), (300, 5000, 528)]
+          (1500, 4099, 1040), (1000, 9001, 1040), (1600, 4099, 384), (2000, 5000, 400), (300, 5000, 528),
+          (430, 9000, 272), (300, 12000, 272), (380, 10000, 400)]
 
 
 def _codes(rows, k, gen):
