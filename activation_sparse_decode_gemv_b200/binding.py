@@ -537,7 +537,8 @@ def pi_block_norm_backward(norm: BlockNorm, x_out: Optional[torch.Tensor], y: Op
                            flags: int = 0, stream=None):
     """Gradients for du [T, d] and dx_out fp32 [T, d] (either may be None): dx
     fp32 [T, d] (may be dx_out), dy [T, d] (may be y), dw_post, dw_pre fp32 [d] and
-    dgate of the gate's shape; each may be left out."""
+    dgate of the gate's shape (gate rows behind the last token's keep what dgate
+    holds); each may be left out."""
     lead = du if du is not None else dx_out
     if lead is None:
         raise ValueError("pi_block_norm_backward needs du or dx_out")

@@ -104,11 +104,9 @@ cudaError_t split_launch(const GM::Args &a, int split, cudaStream_t st) {
 
 // How a product runs.  nt: token columns of a tile; mb: 256-row blocks of a
 // CTA-pair tile; split: 0 = CTA-pair kernel, else the split-K kernel with
-// clusters of that many CTAs; deep: its one-CTA-per-SM form.  nt = 0: none (the
-// device could not be asked).
+// clusters of that many CTAs.  nt = 0: none (the device could not be asked).
 struct Plan {
   int nt, mb, split;
-  bool deep;
   int b_rows() const { return split ? nt : nt / 2; }  // rows of the B box
 };
 
@@ -121,13 +119,15 @@ struct Tilings {
   } t[8];
   double epilogue;
 };
-// 160 to 224 columns waste fewer of the last tile's where tokens are not a multiple of 256
+// 160 to 224 columns waste fewer of the last tile's where tokens are not a
+// multiple of 256: with them 619 tokens of 8128 x 28176 take 681 us, without 741
 constexpr Tilings kGluTilings{5, {{2, 256}, {2, 224}, {2, 192}, {2, 160}, {2, 128}}, 9000};
 constexpr Tilings kDgluTilings{5, {{1, 256}, {1, 224}, {1, 192}, {1, 160}, {1, 128}}, 10000};
 constexpr Tilings kStoreTilings{
     8, {{2, 256}, {2, 224}, {2, 192}, {2, 160}, {1, 256}, {1, 192}, {1, 160}, {1, 128}}, 6000};
 constexpr Tilings kWeightTilings{2, {{2, 256}, {1, 256}}, 6000};
-// {2, 256} measured 10% slower (4096 x 5120 x 13824: 245 us, 224)
+// {2, 256} measured 10% slower (4096 x 5120 x 13824: 245 us, 224); 430 tokens of
+// 4096 x 11008: 28.7 us with 160 to 224 columns, 31.4 without
 constexpr Tilings kI8Tilings{5, {{1, 256}, {1, 224}, {1, 192}, {1, 160}, {1, 128}}, 7000};
 
 // Estimated SM cycles of the two kernels.  A tiling's K blocks cost the slower
@@ -429,8 +429,10 @@ pi_status pi_gated_ffn_forward(pi_gated_ffn_t h, const void *u, int tokens, void
   const pi_status s = ffn_ws(h, tokens, false, ws, ws_bytes, &w);
   if (s != PI_OK) return s;
   const size_t td = (size_t)tokens * h->d.d_model * 2, tf = (size_t)tokens * h->d.d_ffn * 2;
-  const Range r[] = {{y, td}, {gate, tf}, {up, tf}, {ws, ffn_ws_bytes(h, tokens, false)}, {u, td}};
-  if (overlapping(r, 4, 5)) return PI_ERR_INVALID_ARG;
+  const size_t wb = (size_t)h->d.d_ffn * h->d.d_model * 2;
+  const Range r[] = {{y, td}, {gate, tf},        {up, tf},        {ws, ffn_ws_bytes(h, tokens, false)},
+                     {u, td}, {h->d.w_gate, wb}, {h->d.w_up, wb}, {h->d.w_down_t, wb}};
+  if (overlapping(r, 4, 8)) return PI_ERR_INVALID_ARG;
   if (!h->maps_ok) return PI_ERR_CUDA;
   cudaStream_t st = (cudaStream_t)stream;
   return h->d.dtype == PI_DT_F16 ? ffn_forward<__half>(h, u, tokens, y, gate, up, w, st)
@@ -463,9 +465,11 @@ pi_status pi_gated_ffn_backward(pi_gated_ffn_t h, const void *u, const void *gat
   if (s != PI_OK) return s;
   const size_t td = (size_t)tokens * h->d.d_model * 2, tf = (size_t)tokens * h->d.d_ffn * 2;
   const size_t fd = (size_t)h->d.d_ffn * h->d.d_model * type_size(grad_dtype);
-  const Range r[] = {{du, td}, {dw_gate, fd}, {dw_up, fd}, {dw_down_t, fd}, {ws, ffn_ws_bytes(h, tokens, true)},
-                     {u, td},  {gate, tf},    {up, tf},    {dy, td}};
-  if (overlapping(r, 5, 9)) return PI_ERR_INVALID_ARG;
+  const size_t wb = (size_t)h->d.d_ffn * h->d.d_model * 2;
+  const Range r[] = {{du, td},  {dw_gate, fd}, {dw_up, fd},       {dw_down_t, fd}, {ws, ffn_ws_bytes(h, tokens, true)},
+                     {u, td},   {gate, tf},    {up, tf},          {dy, td},        {h->d.w_gate, wb},
+                     {h->d.w_up, wb},          {h->d.w_down_t, wb}};
+  if (overlapping(r, 5, 12)) return PI_ERR_INVALID_ARG;
   if (!h->maps_ok) return PI_ERR_CUDA;
   return h->d.dtype == PI_DT_F16
              ? ffn_backward<__half>(h, u, gate, up, dy, tokens, du, dw_gate, dw_up, dw_down_t, grad_dtype, acc, w, st)

@@ -93,7 +93,7 @@ constexpr int kMaxTokens = 1 << 24;  // tile and row indices stay in 32 bits
 inline int cdiv(int a, int b) { return (a + b - 1) / b; }
 inline bool overlap(const void *p, size_t pn, const void *q, size_t qn) {
   const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
-  return p && q && a < b + qn && b < a + pn;
+  return p && q && pn && qn && a < b + qn && b < a + pn;
 }
 // Memory of an argument (null: none).
 struct Range {

@@ -125,6 +125,10 @@ pi_status bwd_dispatch(const NM::BwdArgs &a, int groups, const RowShape &r, cuda
     return r.rows == 2 ? bwd_launch<4, 2, false>(a, groups, r, st) : bwd_launch<4, 1, false>(a, groups, r, st);
   }
 }
+size_t gate_bytes(const pi_block_norm_desc *D, int tokens) {
+  if (!D->gate || tokens <= 0) return 0;
+  return (size_t)((tokens - 1) / D->tokens_per_gate + 1) * D->d_model * 4;
+}
 size_t norm_ws_bytes(int d, int G) { return kHeader + (size_t)G * d * 4 * 4; }  // dw_post, dw_pre, 2 gate rows
 
 }  // namespace
@@ -143,12 +147,11 @@ pi_status pi_block_norm_forward(const pi_block_norm_desc *desc, const float *x, 
   const void *ptrs[] = {x, y, x_out, u, rstd_post, rstd_pre};
   for (const void *p : ptrs)
     if (p && !aligned16(p)) return PI_ERR_MISALIGNED;
-  const size_t n = (size_t)tokens * desc->d_model;
-  if (x_out != x && overlap(x_out, n * 4, x, n * 4)) return PI_ERR_INVALID_ARG;
-  if (overlap(x_out, n * 4, y, n * type_size(desc->y_dtype)) || overlap(u, n * type_size(desc->u_dtype), x, n * 4) ||
-      overlap(u, n * type_size(desc->u_dtype), x_out, n * 4) ||
-      overlap(u, n * type_size(desc->u_dtype), y, n * type_size(desc->y_dtype)))
-    return PI_ERR_INVALID_ARG;
+  const size_t n = (size_t)tokens * desc->d_model, t4 = (size_t)tokens * 4, d4 = (size_t)desc->d_model * 4;
+  const Range mem[] = {{x_out, n * 4}, {u, n * type_size(desc->u_dtype)}, {rstd_post, t4}, {rstd_pre, t4},
+                       {x_out == x ? nullptr : x, n * 4}, {y, n * type_size(desc->y_dtype)}, {desc->w_post, d4},
+                       {desc->w_pre, d4}, {desc->gate, gate_bytes(desc, tokens)}};
+  if (overlapping(mem, 4, 9)) return PI_ERR_INVALID_ARG;
   NM::FwdArgs a{};
   a.x = x, a.y = y;
   a.w_post = desc->w_post, a.w_pre = desc->w_pre, a.gate = desc->gate;
@@ -194,10 +197,11 @@ pi_status pi_block_norm_backward(const pi_block_norm_desc *desc, const float *x_
     if (p && !aligned16(p)) return PI_ERR_MISALIGNED;
   const int d = desc->d_model;
   const size_t n = (size_t)tokens * d, nx = n * 4, ny = n * type_size(desc->y_dtype), nu = n * type_size(desc->u_dtype);
-  if ((dx != dx_out && overlap(dx, nx, dx_out, nx)) || overlap(dx, nx, x_out, nx) || overlap(dx, nx, y, ny) ||
-      overlap(dx, nx, du, nu) || overlap(dy, ny, x_out, nx) || (dy != y && overlap(dy, ny, y, ny)) ||
-      overlap(dy, ny, du, nu) || overlap(dy, ny, dx_out, nx) || overlap(dx, nx, dy, ny))
-    return PI_ERR_INVALID_ARG;
+  const size_t t4 = (size_t)tokens * 4, d4 = (size_t)d * 4, ng = gate_bytes(desc, tokens);
+  Range mem[] = {{dx, nx}, {dy, ny}, {dw_post, d4}, {dw_pre, d4}, {dgate, ng}, {nullptr, 0}, {x_out, nx},
+                 {dy == y ? nullptr : y, ny}, {rstd_post, t4}, {rstd_pre, t4}, {du, nu},
+                 {dx == dx_out ? nullptr : dx_out, nx}, {desc->w_post, d4}, {desc->w_pre, d4}, {desc->gate, ng}};
+  if (overlapping(mem, 6, 15)) return PI_ERR_INVALID_ARG;
   cudaStream_t st = (cudaStream_t)stream;
   const int acc = (flags & PI_GRAD_ACCUMULATE) ? 1 : 0;
   if (tokens == 0) {  // no tokens: the sums over them are zero (and there is no gate row)
@@ -212,6 +216,8 @@ pi_status pi_block_norm_backward(const pi_block_norm_desc *desc, const float *x_
   const RowShape r = row_shape(d, 8 + (int)type_size(desc->u_dtype) + (int)type_size(desc->y_dtype), true);
   const int G = norm_bwd_groups(row_groups(r, sms), tokens, sms);
   if (ws_bytes < norm_ws_bytes(d, G)) return PI_ERR_WORKSPACE;
+  mem[5] = Range{ws, norm_ws_bytes(d, G)};
+  if (overlapping(mem, 6, 15)) return PI_ERR_INVALID_ARG;
   float *part = reinterpret_cast<float *>(static_cast<char *>(ws) + kHeader);
   NM::BwdArgs a{};
   a.x_out = x_out, a.y = y, a.du = du, a.rstd_post = rstd_post, a.rstd_pre = rstd_pre, a.dx_out = dx_out;

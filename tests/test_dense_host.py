@@ -138,6 +138,39 @@ def test_block_norm_calls(lib):
     assert lib.pi_block_norm_workspace_size(_norm(d_model=4), 1, C.byref(n)) == UNSUP
 
 
+def test_outputs_over_weights_and_parameters(lib):
+    _, h = _gated(lib, w_gate=A.value, w_up=B_.value, w_down_t=C_.value)
+    last = 64 * 128 * 2 - 16  # the last 16 bytes of a weight
+    fwd, ws = lib.pi_gated_ffn_forward, vp(0x9000)
+    for w in (A, B_, C_):
+        p = vp(w.value + last)
+        assert fwd(h, D_, 1, p, None, None, ws, 1 << 20, None) == ARG
+        assert fwd(h, D_, 1, E_, p, None, ws, 1 << 20, None) == ARG
+        assert fwd(h, D_, 1, E_, None, p, ws, 1 << 20, None) == ARG
+        assert fwd(h, D_, 1, E_, None, None, p, 1 << 20, None) == ARG
+        for at in range(4):
+            out = [None] * 4
+            out[at] = p
+            assert lib.pi_gated_ffn_backward(h, D_, E_, F_, G_, 1, *out, pb.PI_DT_F16, 0, ws, 1 << 20, None) == ARG
+    lib.pi_gated_ffn_destroy(h)
+
+    def fwd(r=C_, u=D_, kp=E_, kr=F_):
+        return lib.pi_block_norm_forward(_norm(), A, B_, 4, r, u, kp, kr, None)
+    for w in (0x1000, 0x2000, 0x3000):
+        assert fwd(r=vp(w)) == ARG and fwd(u=vp(w + 240)) == ARG and fwd(kp=vp(w)) == ARG and fwd(kr=vp(w)) == ARG
+    assert fwd(kp=F_) == ARG and fwd(kp=C_) == ARG and fwd(kr=D_) == ARG and fwd(kr=A) == ARG
+
+    def bwd(dx=E_, dy=F_, dwp=G_, dw=H_, dg=vp(0x300), T=4):
+        return lib.pi_block_norm_backward(_norm(), A, B_, vp(0x100), vp(0x200), C_, D_, T, dx, dy, dwp, dw, dg, 0,
+                                          vp(0x9000), 1 << 30, None)
+    for w in (0x1000, 0x2000, 0x3000):
+        p = vp(w + 240)
+        assert bwd(dx=p) == ARG and bwd(dy=p) == ARG and bwd(dwp=p) == ARG and bwd(dw=p) == ARG and bwd(dg=p) == ARG
+    assert bwd(dwp=H_) == ARG and bwd(dw=E_) == ARG and bwd(dg=G_) == ARG and bwd(dwp=A) == ARG and bwd(dw=D_) == ARG
+    assert bwd(dx=vp(0x200)) == ARG and bwd(dw=vp(0x100)) == ARG
+    assert bwd(dg=vp(0x3100), T=5) == ARG  # the gate's second row
+
+
 def test_matmul_i8_calls(lib):
     qz = lib.pi_quantize_i8
     assert qz(None, 0, 4, 64, A, B_, None) == ARG and qz(A, 0, 4, 64, None, C_, None) == ARG

@@ -364,3 +364,15 @@ def test_two_streams_at_once(cuda_device):
     torch.cuda.synchronize()
     for a, b in zip(want, got):
         assert all(torch.equal(a[x], b[x]) for x in a if a[x] is not None)
+
+
+def test_backward_refuses_outputs_in_its_workspace(cuda_device):
+    T, d = 5, 64
+    n = pb.BlockNorm(d, y_dtype=F32, u_dtype=F32)
+    ws = pb.make_block_norm_workspace(n, T)
+    x, kr, g = torch.ones(T, d, device="cuda"), torch.ones(T, device="cuda"), torch.ones(T, d, device="cuda")
+    used = ws.view(torch.float32)
+    dw = used[64:64 + d]  # the first row of partial sums
+    with pytest.raises(pb.PiError):
+        pb.pi_block_norm_backward(n, x, None, None, kr, g, None, torch.empty_like(x), None, ws, dw_pre=dw)
+    assert torch.all(kr == 1)
