@@ -72,6 +72,18 @@ PI_DEV void row_sync() {
     __syncthreads();
   }
 }
+// The blocks of a cluster are launched together, which does not say that the
+// other one has begun: its shared memory may be written only after a barrier
+// that it has passed too.  Arrival at the kernel's start, the wait before the
+// first row's sums, so that the first rows' loads hide it.
+template <bool CL>
+PI_DEV void peer_started_arrive() {
+  if constexpr (CL) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+template <bool CL>
+PI_DEV void peer_started_wait() {
+  if constexpr (CL) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 // Row-wide sums of N values; buf: 32 N floats of shared memory that no warp
 // has read since the last but one barrier (callers alternate two buffers).
 template <int N, bool CL>
@@ -252,6 +264,7 @@ __global__ void __launch_bounds__(512, CH <= 3 ? 2 : 1) norm_fwd_kernel(const Fw
   using U = Part<CH, UT>;
   extern __shared__ __align__(16) unsigned char ring[];
   __shared__ float buf[2][32];
+  peer_started_arrive<CL>();
   const int d = a.d, step = blockDim.x, half = cluster_half<CL>();
   const int dh = CL ? d / 2 : d, col0 = half * dh;  // this block's columns
   const int G = gridDim.x / (CL ? 2 : 1), blk = blockIdx.x / (CL ? 2 : 1);
@@ -288,6 +301,7 @@ __global__ void __launch_bounds__(512, CH <= 3 ? 2 : 1) norm_fwd_kernel(const Fw
     if (!a.gate) bf[c] = factor(nullptr, c);
   }
   const unsigned long long alpha = pk(a.alpha, a.alpha);
+  peer_started_wait<CL>();
   int slot_i = 0;
   for (int t = t0; t < t1; ++t) {
     if (a.gate && t / a.tokens_per_gate != group) {
@@ -404,6 +418,7 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const BwdArgs a) {
   using U = Part<CH, UT>;
   extern __shared__ __align__(16) unsigned char ring[];
   __shared__ float buf[2][96];
+  peer_started_arrive<CL>();
   const int d = a.d, step = blockDim.x, half = cluster_half<CL>();
   const int dh = CL ? d / 2 : d, col0 = half * dh;  // this block's columns
   const int G = gridDim.x / (CL ? 2 : 1), blk = blockIdx.x / (CL ? 2 : 1);
@@ -462,6 +477,7 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const BwdArgs a) {
   };
   const unsigned long long alpha = pk(a.alpha, a.alpha);
   float rr_next = rr_of(t0), rp_next = rp_of(t0);
+  peer_started_wait<CL>();
   int slot_i = 0;
   for (int t = t0; t < t1; ++t) {
     if (a.gate) {
