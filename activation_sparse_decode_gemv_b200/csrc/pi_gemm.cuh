@@ -435,7 +435,7 @@ PI_DEV void dglu_act(const float (&da)[NC], const float (&g)[NC], const float (&
     float phi, slope;
     gate_phi_grad<ACT>(g[j], phi, slope);
     dp[j] = da[j] * phi;
-    dg[j] = da[j] * p[j] * slope;
+    dg[j] = da[j] * slope * p[j];  // da p alone may pass fp32 (bf16 inputs) where phi' is small or zero
     av[j] = phi * p[j];
   }
 }

@@ -96,3 +96,21 @@ def test_activation_and_its_slope(cuda_device, dtype, act, up, tokens):
     c, k = _slope_terms(act, G)
     _within(du[:, 0], (c + k) * up, (c.abs() + k.abs()) * up, dtype, flushed + up * 2.0 ** -125)
     _within(du[:, 1], want / up, want.abs() / up, dtype, flushed + 2.0 ** -125)
+
+
+@pytest.mark.parametrize("tokens", [3, 300])
+@pytest.mark.parametrize("act,at", [("relu", -1.0), ("relu", 0.0), ("silu", -1.28125), ("gelu", -0.75)])
+def test_large_gradients_times_a_small_slope(cuda_device, act, at, tokens):
+    """dg = da p phi'(g) where da p lies past fp32's largest value and phi' is zero or small: dg is finite."""
+    dtype, big = torch.bfloat16, 2.0 ** 66
+    layer = _layer(dtype, act)
+    ws = pb.make_gated_ffn_workspace(layer, tokens, True)
+    u, gate, upo, dy = (torch.zeros(tokens, 8, dtype=dtype, device="cuda") for _ in range(4))
+    gate[:, 0], upo[:, 0], dy[:, 0] = at, big, big
+    du = torch.empty_like(u)
+    pb.pi_gated_ffn_backward(layer, u, gate, upo, dy, ws, du)
+    c, k = _slope_terms(act, gate[:, 0].to(D))
+    want = (c + k) * big * big
+    assert want.abs().max() < 1e38
+    tol = ref.step(dtype) * want.abs() + R * (c.abs() + k.abs()) * big * big
+    assert torch.all((du[:, 0].to(D) - want).abs() <= tol)
