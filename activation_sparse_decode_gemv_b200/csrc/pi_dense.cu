@@ -51,6 +51,9 @@ cudaError_t pair_launch(const GM::Args &a, int sms, cudaStream_t st) {
 // allocates tensor memory the occupancy calculator answers with one CTA per
 // SM, whatever it allocates, but the hardware runs two.
 __global__ void __launch_bounds__(GM::kSplitThreads) shape_kernel() {}
+// The largest of the widths' shapes, so that what the device holds of it, it
+// holds of each.
+constexpr int kSplitSmem = GM::SplitShape<48>::SMEM;
 struct ClusterCaps {
   int n[kMaxSplit + 1];  // by split; 0: does not run
 };
@@ -70,7 +73,7 @@ const ClusterCaps *cluster_caps() {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(split);
     cfg.blockDim = dim3(GM::kSplitThreads);
-    cfg.dynamicSmemBytes = GM::SplitShape<16>::SMEM;  // the largest
+    cfg.dynamicSmemBytes = kSplitSmem;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = (unsigned)split;
@@ -91,6 +94,7 @@ template <int EPI, int AMN, int NT, typename T>
 cudaError_t split_launch(const GM::Args &a, int split, cudaStream_t st) {
   static DeviceOnce once;
   using Sh = GM::SplitShape<NT>;
+  static_assert(Sh::SMEM <= kSplitSmem, "the capacities are asked for a smaller block");
   const auto kern = GM::split_gemm_kernel<EPI, AMN, NT, T>;
   cudaError_t e = once.ensure([&] {
     const cudaError_t r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::SMEM);
