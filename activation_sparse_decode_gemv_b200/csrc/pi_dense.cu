@@ -65,6 +65,7 @@ const ClusterCaps *cluster_caps() {
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return nullptr;
   if (const ClusterCaps *c = ready[dev].load(std::memory_order_acquire)) return c;
   std::lock_guard<std::mutex> lock(mu);
+  if (const ClusterCaps *c = ready[dev].load(std::memory_order_acquire)) return c;  // another thread was first
   if (cudaFuncSetAttribute(shape_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024) != cudaSuccess ||
       cudaFuncSetAttribute(shape_kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
                            cudaSharedmemCarveoutMaxShared) != cudaSuccess)

@@ -1,4 +1,4 @@
-"""Calls from host threads: a thread that has made no CUDA call of its own yet
+"""Calls from host threads.  A thread that has made no CUDA call of its own yet
 (an autograd worker, a server's handler) has no current context, and the calls
 have to work there all the same."""
 import os
@@ -68,3 +68,59 @@ def _child(code):
 @pytest.mark.parametrize("T", [2, 300])
 def test_layers_made_and_called_in_a_thread_without_a_context(cuda_device, T):
     _child(FRESH % T)
+
+
+MANY = """
+import threading, torch
+from activation_sparse_decode_gemv_b200 import binding as pb
+N, d, f, k = 12, 264, 1032, 272
+g = torch.Generator(device="cuda").manual_seed(0)
+n = lambda *s: torch.randn(*s, generator=g, device="cuda")
+pb.lib()
+jobs = []
+for i in range(N):
+    T = (1, 3, 40, 200)[i % 4]
+    w = [(n(f, d) * 0.05).half() for _ in range(3)]
+    layer = pb.GatedFfnLayer(*w)
+    j = {"layer": layer, "ws": pb.make_gated_ffn_workspace(layer, T, True), "u": n(T, d).half(), "dy": n(T, d).half(),
+         "x": n(T, k), "q": torch.empty(T, k, dtype=torch.int8, device="cuda"), "s": torch.empty(T, device="cuda"),
+         "wq": torch.randint(-128, 128, (96, k), generator=g, device="cuda", dtype=torch.int32).to(torch.int8),
+         "one": torch.ones(96, device="cuda"), "iws": pb.make_matmul_i8_workspace(T, 96, k)}
+    j["out"] = [torch.empty(T, m, dtype=torch.half, device="cuda") for m in (d, f, f, d)] + \\
+        [torch.empty(f, d, dtype=torch.half, device="cuda") for _ in range(3)] + [torch.empty(T, 96, device="cuda")]
+    jobs.append(j)
+torch.cuda.synchronize()
+def run(j):
+    y, gate, up, du, *dw, z = j["out"]
+    pb.pi_gated_ffn_forward(j["layer"], j["u"], y, j["ws"], gate=gate, up=up)
+    pb.pi_gated_ffn_backward(j["layer"], j["u"], gate, up, j["dy"], j["ws"], du, *dw)
+    pb.pi_quantize_i8(j["x"], j["q"], j["s"])
+    pb.pi_matmul_i8(j["q"], j["s"], j["wq"], j["one"], z, j["iws"])
+start, errors = threading.Barrier(N), []
+def thread(j):
+    try:
+        with torch.cuda.stream(torch.cuda.Stream()):
+            start.wait()
+            for _ in range(3):
+                run(j)
+            torch.cuda.current_stream().synchronize()
+    except Exception as e:
+        errors.append(e)
+ts = [threading.Thread(target=thread, args=(j,)) for j in jobs]
+[t.start() for t in ts], [t.join() for t in ts]
+assert not errors, errors
+for j in jobs:
+    got = [t.clone() for t in j["out"]]
+    for t in j["out"]:
+        t.zero_()
+    run(j)
+    assert all(torch.equal(a, b) for a, b in zip(got, j["out"]))
+    assert pb.pi_get_device_status(j["ws"]) == 0 and pb.pi_get_device_status(j["iws"]) == 0
+print("threads agree")
+"""
+
+
+def test_first_calls_of_many_threads_at_once(cuda_device):
+    """Each on a stream of its own: what a first call sets up for the device is set up once and read by the
+    others, and every thread's results are those of a call alone."""
+    _child(MANY)
