@@ -154,11 +154,19 @@ def _on_device(**tensors: Optional[torch.Tensor]):
             raise ValueError(f"{what}: must be a CUDA tensor")
 
 
+def _c_int(n, what: str) -> int:
+    """n as a C int, which ctypes would take modulo 2^32."""
+    n = int(n)
+    if not -2 ** 31 <= n < 2 ** 31:
+        raise ValueError(f"{what}: {n}, over 2147483647 in size")
+    return n
+
+
 def _tokens(u: torch.Tensor, d: int, what: str) -> int:
     """Batch size of a [B, d] token tensor."""
     if u.dim() != 2 or u.shape[1] != d:
         raise ValueError(f"{what}: shape {tuple(u.shape)}, expected [B, {d}]")
-    return u.shape[0]
+    return _c_int(u.shape[0], f"{what}: rows")
 
 
 def _need_ws(ws: torch.Tensor):
@@ -419,8 +427,8 @@ class GatedFfnLayer:
 
 def pi_gated_ffn_workspace_size(layer: GatedFfnLayer, max_tokens: int, backward: bool = False) -> int:
     n = C.c_size_t()
-    _check(lib().pi_gated_ffn_workspace_size(layer.handle, int(max_tokens), int(backward), C.byref(n)),
-           "pi_gated_ffn_workspace_size")
+    _check(lib().pi_gated_ffn_workspace_size(layer.handle, _c_int(max_tokens, "max_tokens"), int(bool(backward)),
+                                             C.byref(n)), "pi_gated_ffn_workspace_size")
     return n.value
 
 
@@ -475,20 +483,21 @@ class BlockNorm:
                  residual_scale: float = 1.0, branch_scale: float = 1.0, post_norm: bool = False,
                  w_post: Optional[torch.Tensor] = None, w_pre: Optional[torch.Tensor] = None,
                  gate: Optional[torch.Tensor] = None, tokens_per_gate: int = 0):
+        d, tokens_per_gate = _c_int(d, "d"), _c_int(tokens_per_gate, "tokens_per_gate")
         for what, t in (("y_dtype", y_dtype), ("u_dtype", u_dtype)):
             if t not in DTYPE:
                 raise ValueError(f"{what}: {t}, expected one of {list(DTYPE)}")
         _check_out(w_post, "w_post", torch.float32, (d,))
         _check_out(w_pre, "w_pre", torch.float32, (d,))
         if gate is not None:
-            if gate.dim() != 2 or int(tokens_per_gate) <= 0:
+            if gate.dim() != 2 or tokens_per_gate <= 0:
                 raise ValueError("gate: expected [rows, d] and tokens_per_gate > 0")
             _check_out(gate, "gate", torch.float32, (gate.shape[0], d))
         self.d, self.y_dtype, self.u_dtype, self.post_norm = d, y_dtype, u_dtype, bool(post_norm)
-        self.gate, self.tokens_per_gate = gate, int(tokens_per_gate)
+        self.gate, self.tokens_per_gate = gate, tokens_per_gate
         self.w_post, self.w_pre = w_post, w_pre
         self.desc = pi_block_norm_desc(d, DTYPE[y_dtype], DTYPE[u_dtype], int(post_norm), eps, residual_scale,
-                                       branch_scale, _p(w_post), _p(w_pre), _p(gate), int(tokens_per_gate))
+                                       branch_scale, _p(w_post), _p(w_pre), _p(gate), tokens_per_gate)
         self.ref = C.byref(self.desc)
 
     def _check_tokens(self, T: int):
@@ -519,7 +528,7 @@ def pi_block_norm_forward(norm: BlockNorm, x: torch.Tensor, y: Optional[torch.Te
 
 def pi_block_norm_workspace_size(norm: BlockNorm, max_tokens: int) -> int:
     n = C.c_size_t()
-    _check(lib().pi_block_norm_workspace_size(norm.ref, int(max_tokens), C.byref(n)),
+    _check(lib().pi_block_norm_workspace_size(norm.ref, _c_int(max_tokens, "max_tokens"), C.byref(n)),
            "pi_block_norm_workspace_size")
     return n.value
 
@@ -567,7 +576,7 @@ def pi_quantize_i8(x: torch.Tensor, q: torch.Tensor, scales: torch.Tensor, strea
     """Rows of x [rows, k] (fp32, fp16 or bf16) -> int8 codes q [rows, k] and fp32 scales [rows]."""
     if x.dim() != 2 or x.dtype not in DTYPE:
         raise ValueError(f"x: {x.dtype} of shape {tuple(x.shape)}, expected fp32, fp16 or bf16 [rows, k]")
-    rows, k = x.shape
+    rows, k = _c_int(x.shape[0], "x: rows"), _c_int(x.shape[1], "x: columns")
     _check_out(x, "x", x.dtype, (rows, k))
     _check_out(q, "q", torch.int8, (rows, k))
     _check_out(scales, "scales", torch.float32, (rows,))
@@ -577,7 +586,7 @@ def pi_quantize_i8(x: torch.Tensor, q: torch.Tensor, scales: torch.Tensor, strea
 
 def pi_matmul_i8_workspace_size(tokens: int, n: int, k: int) -> int:
     size = C.c_size_t()
-    _check(lib().pi_matmul_i8_workspace_size(int(tokens), int(n), int(k), C.byref(size)),
+    _check(lib().pi_matmul_i8_workspace_size(_c_int(tokens, "tokens"), _c_int(n, "n"), _c_int(k, "k"), C.byref(size)),
            "pi_matmul_i8_workspace_size")
     return size.value
 
@@ -595,7 +604,7 @@ def pi_matmul_i8(xq: torch.Tensor, x_scales: torch.Tensor, wq: torch.Tensor, w_s
         raise ValueError(f"xq {tuple(xq.shape)} and wq {tuple(wq.shape)}: expected [T, k] and [n, k]")
     if y.dtype not in DTYPE:
         raise ValueError(f"y: dtype {y.dtype}, expected one of {list(DTYPE)}")
-    (T, k), n = xq.shape, wq.shape[0]
+    T, k, n = _c_int(xq.shape[0], "xq: rows"), _c_int(xq.shape[1], "xq: columns"), _c_int(wq.shape[0], "wq: rows")
     _check_out(xq, "xq", torch.int8, (T, k))
     _check_out(wq, "wq", torch.int8, (n, k))
     _check_out(x_scales, "x_scales", torch.float32, (T,))
