@@ -358,6 +358,14 @@ def _ptrs(names: str, *tensors: Optional[torch.Tensor]):
     return out
 
 
+def _check_moved(names, tensors, at):
+    """The tensors whose addresses a handle or a description holds still lie there: their values may change in
+    place, but one that was given other memory (w.data = ...) would be read where it was."""
+    for what, t, p in zip(names, tensors, at):
+        if t is not None and t.data_ptr() != p:
+            raise ValueError(f"{what}: its memory has moved since the layer or norm was made; make a new one")
+
+
 def _check_device(names: str, tensors, d: int) -> int:
     """Device d of one of the tensors, if it is the current one."""
     if d < 0 or d != torch.cuda.current_device():
@@ -407,11 +415,15 @@ class GatedFfnLayer:
             if t.device != w_gate.device:
                 raise ValueError(f"{what}: on {t.device}, w_gate is on {w_gate.device}")
         self._keep = (w_gate, w_up, w_down_t)
+        self._at = tuple(t.data_ptr() for t in self._keep)
         self.desc = pi_gated_ffn_desc(self.d, self.f, GATE_ACT[act], DTYPE[self.dtype], _p(w_gate), _p(w_up),
                                       _p(w_down_t))
         h = C.c_void_p()
         _check(lib().pi_gated_ffn_create(C.byref(self.desc), C.byref(h)), "pi_gated_ffn_create")
         self.handle = h
+
+    def _check_weights(self):
+        _check_moved(("w_gate", "w_up", "w_down_t"), self._keep, self._at)
 
     def close(self):
         if getattr(self, "handle", None):
@@ -441,6 +453,7 @@ def pi_gated_ffn_forward(layer: GatedFfnLayer, u: torch.Tensor, y: torch.Tensor,
                          gate: Optional[torch.Tensor] = None, up: Optional[torch.Tensor] = None, stream=None):
     """u [T, d] -> y [T, d]; gate, up: optional outputs [T, f] (the pre-activations)."""
     T = _tokens(u, layer.d, "u")
+    layer._check_weights()
     _check_out(u, "u", layer.dtype, (T, layer.d))
     _check_out(y, "y", layer.dtype, (T, layer.d))
     _check_out(gate, "gate", layer.dtype, (T, layer.f))
@@ -458,6 +471,7 @@ def pi_gated_ffn_backward(layer: GatedFfnLayer, u: torch.Tensor, gate: torch.Ten
     """Gradients at a forward call's u, gate and up, for dy [T, d].  du [T, d];
     dw_* [f, d], all fp32 or all of the layer's type; each may be left out."""
     T = _tokens(u, layer.d, "u")
+    layer._check_weights()
     for what, t in (("u", u), ("dy", dy), ("du", du)):
         _check_out(t, what, layer.dtype, (T, layer.d))
     for what, t in (("gate", gate), ("up", up)):
@@ -496,12 +510,14 @@ class BlockNorm:
         self.d, self.y_dtype, self.u_dtype, self.post_norm = d, y_dtype, u_dtype, bool(post_norm)
         self.gate, self.tokens_per_gate = gate, tokens_per_gate
         self.w_post, self.w_pre = w_post, w_pre
+        self._at = tuple(None if t is None else t.data_ptr() for t in (w_post, w_pre, gate))
         self.desc = pi_block_norm_desc(d, DTYPE[y_dtype], DTYPE[u_dtype], int(post_norm), eps, residual_scale,
                                        branch_scale, _p(w_post), _p(w_pre), _p(gate), tokens_per_gate)
         self.ref = C.byref(self.desc)
 
     def _check_tokens(self, T: int):
-        """The gate has a row for each of T tokens."""
+        """The gate has a row for each of T tokens, and the parameters lie where they did."""
+        _check_moved(("w_post", "w_pre", "gate"), (self.w_post, self.w_pre, self.gate), self._at)
         if self.gate is not None and self.gate.shape[0] * self.tokens_per_gate < T:
             raise ValueError(f"gate: {self.gate.shape[0]} rows of {self.tokens_per_gate} tokens for {T} tokens")
 

@@ -58,3 +58,33 @@ def test_tensors_of_more_rows_than_a_c_int():
                                          e(1, BIG, dt=torch.float32), ws)):
         with pytest.raises(ValueError, match="over 2147483647"):
             call()
+
+
+def test_weights_and_parameters_whose_memory_moved():
+    """A layer and a norm hold addresses.  A tensor given other memory since (w.data = ..., set_) would be read where
+    it was: freed memory.  New values in the same memory are fine."""
+    h = torch.float16
+    u, ws = torch.zeros(4, 64, dtype=h), torch.zeros(65536, dtype=torch.uint8)
+    g, f, s = torch.zeros(4, 128, dtype=h), torch.zeros(4, 64), torch.zeros(4)
+    for at, name in enumerate(("w_gate", "w_up", "w_down_t")):
+        w = [torch.zeros(128, 64, dtype=h) for _ in range(3)]
+        layer = pb.GatedFfnLayer(*w)
+        w[at].add_(1)
+        with pytest.raises(ValueError, match="must be a CUDA tensor"):  # nothing else is wrong
+            pb.pi_gated_ffn_forward(layer, u, u.clone(), ws)
+        w[at].data = w[at].data.clone()
+        with pytest.raises(ValueError, match=f"{name}: .*moved"):
+            pb.pi_gated_ffn_forward(layer, u, u.clone(), ws)
+        with pytest.raises(ValueError, match=f"{name}: .*moved"):
+            pb.pi_gated_ffn_backward(layer, u, g, g, u, ws)
+    for name in ("w_post", "w_pre", "gate"):
+        p = {"w_post": torch.ones(64), "w_pre": torch.ones(64), "gate": torch.ones(4, 64)}
+        norm = pb.BlockNorm(64, post_norm=True, **p, tokens_per_gate=1)
+        p[name].add_(1)
+        with pytest.raises(ValueError, match="must be a CUDA tensor"):
+            pb.pi_block_norm_forward(norm, f, u, f, u.clone())
+        p[name].data = p[name].data.clone()
+        with pytest.raises(ValueError, match=f"{name}: .*moved"):
+            pb.pi_block_norm_forward(norm, f, u, f, u.clone())
+        with pytest.raises(ValueError, match=f"{name}: .*moved"):
+            pb.pi_block_norm_backward(norm, f, u, s, s, u.clone(), None, f.clone(), u.clone(), ws)
