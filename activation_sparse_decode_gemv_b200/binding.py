@@ -41,7 +41,8 @@ EXPORTS = ("pi_ffn_create", "pi_ffn_destroy", "pi_workspace_size", "pi_workspace
            "pi_get_device_status", "pi_status_string",
            "pi_gated_ffn_create", "pi_gated_ffn_destroy", "pi_gated_ffn_workspace_size", "pi_gated_ffn_forward",
            "pi_gated_ffn_backward", "pi_block_norm_forward", "pi_block_norm_workspace_size",
-           "pi_block_norm_backward", "pi_quantize_i8", "pi_matmul_i8_workspace_size", "pi_matmul_i8")
+           "pi_block_norm_backward", "pi_quantize_i8", "pi_matmul_i8_workspace_size", "pi_matmul_i8",
+           "pi_debug_dense_plan")
 
 
 class PiError(RuntimeError):
@@ -108,9 +109,11 @@ def lib() -> C.CDLL:
         L.pi_quantize_i8.argtypes = [vp, i, i, i, vp, vp, vp]
         L.pi_matmul_i8_workspace_size.argtypes = [i, i, i, C.POINTER(sz)]
         L.pi_matmul_i8.argtypes = [vp, vp, vp, vp, vp, i, i, i, vp, i, vp, sz, vp]
+        L.pi_debug_dense_plan.argtypes = [i, i, i, i]
         for n in ("pi_gated_ffn_create", "pi_gated_ffn_workspace_size", "pi_gated_ffn_forward",
                   "pi_gated_ffn_backward", "pi_block_norm_forward", "pi_block_norm_workspace_size",
-                  "pi_block_norm_backward", "pi_quantize_i8", "pi_matmul_i8_workspace_size", "pi_matmul_i8"):
+                  "pi_block_norm_backward", "pi_quantize_i8", "pi_matmul_i8_workspace_size", "pi_matmul_i8",
+                  "pi_debug_dense_plan"):
             getattr(L, n).restype = C.c_int
         for n in ("pi_ffn_create", "pi_workspace_size", "pi_workspace_init", "pi_predict", "pi_sparse_ffn",
                   "pi_decode_ffn", "pi_decode_ffn_stack", "pi_decode_ffn_static", "pi_debug_wait_fault",
@@ -632,3 +635,9 @@ def pi_matmul_i8(xq: torch.Tensor, x_scales: torch.Tensor, wq: torch.Tensor, w_s
                                           y, ws)
     _check(lib().pi_matmul_i8(pq, ps, pwq, pws, pb_, T, n, k, py, DTYPE[y.dtype], pw, size, _raw_stream(stream)),
            "pi_matmul_i8")
+
+
+def pi_debug_dense_plan(product: int, mb: int = 0, nt: int = 0, split: int = 0):
+    """Test support: a dense product's following calls use this tiling (see
+    the header); product -1 alone restores the rule for all."""
+    _check(lib().pi_debug_dense_plan(int(product), int(mb), int(nt), int(split)), "pi_debug_dense_plan")

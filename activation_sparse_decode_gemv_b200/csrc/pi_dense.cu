@@ -107,6 +107,9 @@ cudaError_t split_launch(const GM::Args &a, int split, cudaStream_t st) {
   return launch1(kern, dim3((unsigned)(a.mt * a.nt * split)), GM::kSplitThreads, Sh::SMEM, split, nullptr, st, a);
 }
 
+// The products of this file, each with tilings of its own.
+enum Product { P_GLU, P_STORE, P_DGLU, P_WEIGHT, P_I8, kProducts };
+
 // How a product runs.  nt: token columns of a tile; mb: 256-row blocks of a
 // CTA-pair tile; split: 0 = CTA-pair kernel, else the split-K kernel with
 // clusters of that many CTAs.  nt = 0: none (the device could not be asked).
@@ -134,6 +137,21 @@ constexpr Tilings kWeightTilings{2, {{2, 256}, {1, 256}}, 6000};
 // {2, 256} measured 10% slower (4096 x 5120 x 13824: 245 us, 224); 430 tokens of
 // 4096 x 11008: 28.7 us with 160 to 224 columns, 31.4 without
 constexpr Tilings kI8Tilings{5, {{1, 256}, {1, 224}, {1, 192}, {1, 160}, {1, 128}}, 7000};
+
+const Tilings &tilings_of(int product) {
+  static const Tilings *const all[kProducts] = {&kGluTilings, &kStoreTilings, &kDgluTilings, &kWeightTilings,
+                                                &kI8Tilings};
+  return *all[product];
+}
+// Token columns of the split kernel's tiles, and its cluster sizes: those of 3
+// and 7 leave SMs with one CTA where others have two (333 tokens, 1032 x 2760,
+// 66 tiles: 15.5 us split by 3, 13.2 by 4; 40 tiles of K 13824: 83.8 us by 7,
+// 70.5 by 6).
+constexpr int kSplitColumns[] = {16, 32, 48, 64, 128};
+constexpr int kSplits[] = {1, 2, 4, 5, 6, 8};
+
+// Test support (pi_debug_dense_plan): the tiling that a product's calls use; nt = 0: the rule's.
+Plan g_forced[kProducts];
 
 // Estimated SM cycles of the two kernels.  A tiling's K blocks cost the slower
 // of the MMAs (2 cycles a column and block), the arrival of its bytes at the
@@ -167,7 +185,9 @@ double split_cost(long long tiles, int ntn, int kb, int nt, int split, int cap) 
 }
 
 // m_rows: features of a 128-row block (64 for the gate | up product).
-Plan choose(int m, int m_rows, int n, int kb, int sms, const Tilings &tilings) {
+Plan choose(Product product, int m, int m_rows, int n, int kb, int sms) {
+  if (const Plan &p = g_forced[product]; p.nt) return p.split > 1 && p.split * 2 > kb ? Plan{} : p;
+  const Tilings &tilings = tilings_of(product);
   Plan best{};
   double cost = 0;
   const ClusterCaps *caps = cluster_caps();
@@ -180,14 +200,13 @@ Plan choose(int m, int m_rows, int n, int kb, int sms, const Tilings &tilings) {
                                  tilings.epilogue, glu);
       if (cost == 0 || c < cost) cost = c, best = Plan{t.nt, t.mb, 0};
     }
-  for (const int nt : {16, 32, 48, 64, 128}) {
+  for (const int nt : kSplitColumns) {
     const long long tiles = (long long)cdiv(m, m_rows) * cdiv(n, nt);
     if (tiles > 65536) continue;
-    for (int split = 1; split <= kMaxSplit && (split == 1 || split * 2 <= kb); ++split) {
+    for (const int split : kSplits) {
+      if (split > 1 && split * 2 > kb) break;
       const int cap = caps->n[split];
-      // clusters of 3 and 7 leave SMs with one CTA where others have two: 333 tokens, 1032 x 2760 (66
-      // tiles) 15.5 us split by 3, 13.2 by 4; 40 tiles of K 13824 83.8 us by 7, 70.5 by 6
-      if (cap <= 0 || split == 3 || split == 7) continue;
+      if (cap <= 0) continue;
       const double c = split_cost(tiles, cdiv(n, nt), kb, nt, split, cap);
       if (cost == 0 || c < cost) cost = c, best = Plan{nt, 1, split};
     }
@@ -279,7 +298,7 @@ pi_status ffn_forward(const pi_gated_ffn *h, const void *u, int tokens, void *y,
     GM::Args a{};
     a.m = f, a.n = tokens, a.nprob = 1;
     a.kb = a.kb_seg = cdiv(d, 64);
-    const Plan p = choose(f, 64, tokens, a.kb, sms, kGluTilings);
+    const Plan p = choose(P_GLU, f, 64, tokens, a.kb, sms);
     a.ma[0] = p.split ? h->gate64 : h->gate128, a.ma[1] = p.split ? h->up64 : h->up128;
     if (!map16(&a.mb[0], u, tokens, d, p.b_rows())) return PI_ERR_CUDA;
     a.out[0] = w.a;
@@ -292,7 +311,7 @@ pi_status ffn_forward(const pi_gated_ffn *h, const void *u, int tokens, void *y,
   GM::Args a{};
   a.m = d, a.n = tokens, a.nprob = 1;
   a.kb = a.kb_seg = cdiv(f, 64);
-  const Plan p = choose(d, 128, tokens, a.kb, sms, kStoreTilings);
+  const Plan p = choose(P_STORE, d, 128, tokens, a.kb, sms);
   a.ma[0] = h->down64;
   if (!map16(&a.mb[0], w.a, tokens, f, p.b_rows())) return PI_ERR_CUDA;
   a.out[0] = y;
@@ -316,7 +335,7 @@ pi_status ffn_backward(const pi_gated_ffn *h, const void *u, const void *gate, c
     GM::Args a{};
     a.m = f, a.n = tokens, a.nprob = 1;
     a.kb = a.kb_seg = cdiv(d, 64);
-    const Plan p = choose(f, 128, tokens, a.kb, sms, kDgluTilings);
+    const Plan p = choose(P_DGLU, f, 128, tokens, a.kb, sms);
     a.ma[0] = h->down128;
     if (!map16(&a.mb[0], dy, tokens, d, p.b_rows())) return PI_ERR_CUDA;
     if (!p.split && (!map_2d(&a.ma[1], gate, true, (uint64_t)f, (uint64_t)tokens, 128, (uint32_t)p.nt, false) ||
@@ -361,6 +380,7 @@ pi_status ffn_backward(const pi_gated_ffn *h, const void *u, const void *gate, c
                                    kWeightTilings.epilogue, false);
         if (i == 0 || c < best) best = c, mb = t.mb;
       }
+      if (g_forced[P_WEIGHT].nt) mb = g_forced[P_WEIGHT].mb;
       a.mt = cdiv(d, 256 * mb);
       a.nt = cdiv(f, 256);
       a.idesc = idesc(dt, false, 256, 256, 1, 1);
@@ -374,7 +394,7 @@ pi_status ffn_backward(const pi_gated_ffn *h, const void *u, const void *gate, c
     a.m = d, a.n = tokens, a.nprob = 1;
     a.kb_seg = cdiv(f, 64);
     a.kb = 2 * a.kb_seg;
-    const Plan p = choose(d, 128, tokens, a.kb, sms, kStoreTilings);
+    const Plan p = choose(P_STORE, d, 128, tokens, a.kb, sms);
     a.ma[0] = h->gate64, a.ma[1] = h->up64;
     if (!map16(&a.mb[0], w.dg, tokens, f, p.b_rows()) || !map16(&a.mb[1], w.dp, tokens, f, p.b_rows()))
       return PI_ERR_CUDA;
@@ -482,6 +502,28 @@ pi_status pi_gated_ffn_backward(pi_gated_ffn_t h, const void *u, const void *gat
                                            w, st);
 }
 
+// ====================================================================== test support
+pi_status pi_debug_dense_plan(int product, int mb, int nt, int split) {
+  if (product == -1 && !mb && !nt && !split) {
+    for (Plan &p : g_forced) p = Plan{};
+    return PI_OK;
+  }
+  if (product < 0 || product >= kProducts) return PI_ERR_INVALID_ARG;
+  bool built = false;
+  if (split == 0) {
+    const Tilings &t = tilings_of(product);
+    for (int i = 0; i < t.n; ++i) built |= t.t[i].mb == mb && t.t[i].nt == nt;
+  } else if (product != P_WEIGHT && mb == 1) {
+    bool columns = false, size = false;
+    for (const int c : kSplitColumns) columns |= c == nt;
+    for (const int c : kSplits) size |= c == split;
+    built = columns && size;
+  }
+  if (!built) return PI_ERR_INVALID_ARG;
+  g_forced[product] = Plan{nt, mb, split};
+  return PI_OK;
+}
+
 // ====================================================================== 8-bit product
 pi_status pi_matmul_i8_workspace_size(int tokens, int n, int k, size_t *bytes) {
   if (!bytes || n <= 0 || k <= 0) return PI_ERR_INVALID_ARG;
@@ -512,7 +554,7 @@ pi_status pi_matmul_i8(const int8_t *xq, const float *x_scales, const int8_t *wq
   GM::Args a{};
   a.m = n, a.n = tokens, a.nprob = 1;
   a.kb = a.kb_seg = cdiv(k, 128);
-  const Plan p = choose(n, 128, tokens, a.kb, sms, kI8Tilings);
+  const Plan p = choose(P_I8, n, 128, tokens, a.kb, sms);
   if (!map_2d(&a.ma[0], wq, false, (uint64_t)k, (uint64_t)n, 128, 128, true) ||
       !map_2d(&a.mb[0], xq, false, (uint64_t)k, (uint64_t)tokens, 128, (uint32_t)p.b_rows(), true))
     return PI_ERR_CUDA;

@@ -346,6 +346,18 @@ pi_status pi_matmul_i8(const int8_t *xq, const float *x_scales, const int8_t *wq
                        const float *bias, int tokens, int n, int k, void *y, int y_dtype, void *ws, size_t ws_bytes,
                        pi_stream_t stream);
 
+/* Test support for the dense products; not part of the path.  A product is
+ * tiled by a rule on its sizes; this makes one product's following calls in
+ * this process use the given tiling, so that each can be tested at any size.
+ * product: 0 gate and up, 1 y and du, 2 da, 3 the weights' gradients, 4 the
+ * 8-bit product.  split = 0: tiles of mb 256-feature blocks by nt tokens on CTA
+ * pairs; else tiles of 128 features by nt tokens, K split over `split` blocks
+ * (mb = 1; K needs 64 x 2 x split elements, 128 x 2 x split in 8 bits).  (-1,
+ * 0, 0, 0) restores the rule for all.  PI_ERR_INVALID_ARG for a tiling that
+ * the product does not have.  Not thread-safe; set it while no call is
+ * running. */
+pi_status pi_debug_dense_plan(int product, int mb, int nt, int split);
+
 /* Synchronise the stream, read and clear the workspace status word.  *code is
  * PI_OK or the first device-side error recorded since the last read. */
 pi_status pi_get_device_status(void *ws, pi_stream_t stream, int *code);
