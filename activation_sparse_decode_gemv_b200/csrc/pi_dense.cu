@@ -238,9 +238,15 @@ cudaError_t pair_dispatch(const GM::Args &a, int nt, int sms, cudaStream_t st) {
   }
 }
 
+void set_waits(GM::Args &a) {
+  a.wait_ns = g_wait_fault.limit_ns ? g_wait_fault.limit_ns : pi::tc::kWaitNs;
+  a.withhold = g_wait_fault.withhold >= 0;
+}
+
 template <int EPI, int AMN, typename T>
 cudaError_t run_plan(GM::Args &a, const Plan &p, int dtype, int m_rows, int sms, cudaStream_t st) {
   if (!p.nt) return cudaErrorUnknown;
+  set_waits(a);
   a.mt = cdiv(a.m, p.split ? m_rows : 2 * p.mb * m_rows);
   a.nt = cdiv(a.n, p.nt);
   a.idesc = idesc(dtype, EPI == GM::E_I8, p.split ? 128 : 256, p.nt, AMN, 0);
@@ -381,6 +387,7 @@ pi_status ffn_backward(const pi_gated_ffn *h, const void *u, const void *gate, c
         if (i == 0 || c < best) best = c, mb = t.mb;
       }
       if (g_forced[P_WEIGHT].nt) mb = g_forced[P_WEIGHT].mb;
+      set_waits(a);
       a.mt = cdiv(d, 256 * mb);
       a.nt = cdiv(f, 256);
       a.idesc = idesc(dt, false, 256, 256, 1, 1);

@@ -344,15 +344,6 @@ bool want_dense(const pi_ffn *h, int B, unsigned flags) {
   return 1.0 - std::pow(1.0 - (p < 1.0 ? p : 1.0), (double)B) >= 0.75;
 }
 
-// Test support (pi_debug_wait_fault): an entry of h that is never published,
-// and a shorter limit for every bounded wait of the fused and batch
-// kernels.
-struct WaitFault {
-  int withhold = -1;
-  unsigned long long limit_ns = 0;  // 0: the kernel's default
-};
-WaitFault g_wait_fault;
-
 // The tensor-core predictor kernels of batches 2..8: fp16 predictor, rank a
 // multiple of 64 up to 1024, d a multiple of 64 up to 8192, P1 and P2 on
 // 32-byte boundaries (256-bit row loads).

@@ -78,6 +78,8 @@ struct Args {
   const float *s_n, *s_m, *bias;  // E_I8
   int early_a;       // split kernel: A was written before the previous kernel; load it before that one ends
   int *status;
+  unsigned long long wait_ns;  // bound of every mbarrier wait
+  int withhold;      // test support: finished accumulators are not announced, so that the waits for them run out
 };
 
 // ---------------------------------------------------------------- PTX: clusters and CTA pairs
@@ -117,23 +119,27 @@ PI_DEV bool mbar_try_cluster(uint64_t *b, unsigned parity, unsigned hint_ns) {
       : "memory");
   return ok != 0;
 }
-// bounded wait on a barrier that the other CTA of the pair may complete
-static __device__ __noinline__ bool mbar_wait_cluster_slow(uint64_t *b, unsigned parity, volatile int *abort_flag,
-                                                           int *status) {
+// Bounded waits, by a.wait_ns: on a barrier that the other CTA of the pair may
+// complete (CLUSTER), or this CTA's own.  A wait that gives up records a
+// timeout and makes the CTA's other roles give up too.
+template <bool CLUSTER>
+__device__ __noinline__ bool wait_slow(uint64_t *b, unsigned parity, volatile int *abort_flag, const Args *a) {
   const unsigned long long t0 = now_ns();
   for (;;) {
-    if (mbar_try_cluster(b, parity, 20000u)) return true;
+    if (CLUSTER ? mbar_try_cluster(b, parity, 20000u) : mbar_try(b, parity, 20000u)) return true;
     if (*abort_flag) return false;
-    if (now_ns() - t0 > kWaitNs) {
-      set_status(status, kStatusTimeout);
+    if (now_ns() - t0 > a->wait_ns) {
+      set_status(a->status, kStatusTimeout);
       *abort_flag = 1;
       return false;
     }
   }
 }
-PI_DEV bool mbar_wait_cluster(uint64_t *b, unsigned parity, volatile int *abort_flag, int *status) {
-  if (mbar_try_cluster(b, parity, 0u)) return true;
-  return mbar_wait_cluster_slow(b, parity, abort_flag, status);
+PI_DEV bool wait_cluster(uint64_t *b, unsigned parity, volatile int *abort_flag, const Args &a) {
+  return mbar_try_cluster(b, parity, 0u) || wait_slow<true>(b, parity, abort_flag, &a);
+}
+PI_DEV bool wait_own(uint64_t *b, unsigned parity, volatile int *abort_flag, const Args &a) {
+  return mbar_test(b, parity) || wait_slow<false>(b, parity, abort_flag, &a);
 }
 
 // TMA load into this CTA's shared memory that completes on a barrier of
@@ -617,7 +623,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           }
         }
         for (int kb = 0; kb < a.kb; ++kb) {
-          if (it >= S::NS && !mbar_wait_cluster(&C.empty[s], ph ^ 1u, abort_flag, a.status)) {
+          if (it >= S::NS && !wait_cluster(&C.empty[s], ph ^ 1u, abort_flag, a)) {
             ok = false;
             break;
           }
@@ -646,7 +652,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       // the MMAs that read the last stages have finished before this CTA may go
       for (int j = 0; j < it && ok; ++j) {
         if (--s < 0) s = S::NS - 1, ph ^= 1u;
-        ok = mbar_wait_cluster(&C.empty[s], ph, abort_flag, a.status);
+        ok = wait_cluster(&C.empty[s], ph, abort_flag, a);
       }
     }
     __syncwarp();
@@ -656,10 +662,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       int tc = 0, s = 0;
       unsigned ph = 0;
       bool ok = true;
-      auto wait_full = [&](int st, unsigned p) { return mbar_wait_cluster(&C.full[st], p, abort_flag, a.status); };
+      auto wait_full = [&](int st, unsigned p) { return wait_cluster(&C.full[st], p, abort_flag, a); };
       auto wait_free = [&](int b) {
         const bool r = tc < S::BUFS ||
-                       mbar_wait_cluster(&C.accfree[buf_of(tc, b)], par_of(tc) ^ 1u, abort_flag, a.status);
+                       wait_cluster(&C.accfree[buf_of(tc, b)], par_of(tc) ^ 1u, abort_flag, a);
         tc_fence_after();
         return r;
       };
@@ -683,7 +689,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             mma_commit_pair(&C.empty[s]);
             if (++s == S::NS) s = 0, ph ^= 1u;
           }
-          if (ok)
+          if (ok && !a.withhold)
 #pragma unroll
             for (int b = 0; b < MB; ++b) mma_commit_pair(&C.accfull[buf_of(tc, b)]);
         } else {
@@ -702,7 +708,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
               issue(0, s0, first && i == 0);
               if (++s0 == S::NS) s0 = 0, p0 ^= 1u;
             }
-            if (last) mma_commit_pair(&C.accfull[0]);
+            if (last && !a.withhold) mma_commit_pair(&C.accfull[0]);
             if (first && !(ok = wait_free(1))) return;
             for (int i = 0; i < n; ++i) {
               issue(1, s, first && i == 0);
@@ -715,7 +721,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           both(head, true, tail == 0);
           while (ok && kb < a.kb - tail) both(1, false, false);
           if (ok && tail) both(tail, false, true);
-          if (ok) mma_commit_pair(&C.accfull[1]);
+          if (ok && !a.withhold) mma_commit_pair(&C.accfull[1]);
         }
       }
     }
@@ -726,7 +732,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     int tc = 0;
     bool go = true;
     auto wait_acc = [&](int b) {
-      const bool r = __all_sync(0xffffffffu, mbar_wait_cluster(&C.accfull[b], par_of(tc), abort_flag, a.status));
+      const bool r = __all_sync(0xffffffffu, wait_cluster(&C.accfull[b], par_of(tc), abort_flag, a));
       tc_fence_after();
       return r;
     };
@@ -913,7 +919,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2) split_gemm_kernel(const __gr
       for (int kb = k0 + first; kb < k1; ++kb) {
         const int i = kb - k0, s = i % S::NS;
         const unsigned ph = (unsigned)((i / S::NS) & 1);
-        if (!mbar_wait(&C.empty[s], ph ^ 1u, abort_flag, a.status)) break;
+        if (!wait_own(&C.empty[s], ph ^ 1u, abort_flag, a)) break;
         start_a(kb, s);
         start_b(kb, s);
       }
@@ -925,7 +931,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2) split_gemm_kernel(const __gr
       bool ok = true;
       for (int kb = k0; kb < k1; ++kb) {
         const int i = kb - k0, s = i % S::NS;
-        if (!mbar_wait(&C.full[s], (unsigned)((i / S::NS) & 1), abort_flag, a.status)) {
+        if (!wait_own(&C.full[s], (unsigned)((i / S::NS) & 1), abort_flag, a)) {
           ok = false;
           break;
         }
@@ -936,14 +942,14 @@ __global__ void __launch_bounds__(kSplitThreads, 2) split_gemm_kernel(const __gr
           mma<1, I8>(tmem, operand_desc<AMN>(st, j), operand_desc<0>(st + S::ABYTES, j), a.idesc, (i | j) ? 1u : 0u);
         mma_commit(&C.empty[s]);
       }
-      if (ok) mma_commit(&C.accfull[0]);
+      if (ok && !a.withhold) mma_commit(&C.accfull[0]);
     }
     __syncwarp();
   } else {
     // ------------------------------------------------------------ partial tile to shared memory
     const int q = warp & 3;
     float *red = reinterpret_cast<float *>(smem);
-    fine = mbar_wait_warp(&C.accfull[0], 0u, abort_flag, a.status);
+    fine = __all_sync(0xffffffffu, wait_own(&C.accfull[0], 0u, abort_flag, a));
     if (fine) {
       tc_fence_after();
       const int nv = min(NT, a.n - col0);

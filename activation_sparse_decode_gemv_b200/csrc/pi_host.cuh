@@ -50,6 +50,16 @@ inline int device_sm_count() {
   return n;
 }
 
+// Test support (pi_debug_wait_fault): an entry of h that is never published (or,
+// for the dense products, finished accumulators that are never announced),
+// and a shorter limit for every bounded wait of the fused, batch and dense
+// kernels.
+struct WaitFault {
+  int withhold = -1;
+  unsigned long long limit_ns = 0;  // 0: the kernel's default
+};
+inline WaitFault g_wait_fault;
+
 // cuTensorMapEncodeTiled through the runtime's driver entry point (no link
 // against the driver library); null when no driver is present.
 using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,

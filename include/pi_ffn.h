@@ -216,12 +216,14 @@ pi_status pi_decode_ffn_static(pi_ffn_t h, const void *u, float *y, int32_t *idx
                                int *dev_status, pi_stream_t stream);
 
 /* Test support for the device-side failure reporting; not part of the decode
- * path (the pages have no counterpart).  It makes the following batch-1 fused
- * launches of this process exercise their bounded waits without any fault:
- * entry withhold_row of the predictor's h (0 <= withhold_row < rank) is never
- * published, so every CTA's wait for h runs out after limit_us microseconds;
- * each launch then records PI_ERR_TIMEOUT in the workspace status word and
- * completes (its outputs are unspecified).  withhold_row = -1 with
+ * path (the pages have no counterpart).  It makes the following launches of
+ * this process exercise their bounded waits without any fault.  Batch-1 fused
+ * launches: entry withhold_row of the predictor's h (0 <= withhold_row < rank)
+ * is never published, so every CTA's wait for h runs out after limit_us
+ * microseconds.  Dense products (any withhold_row >= 0): finished accumulators
+ * are never announced, so the waits for them run out alike.  Each such launch
+ * records PI_ERR_TIMEOUT in the workspace status word and completes (its
+ * outputs are unspecified).  withhold_row = -1 with
  * limit_us = 0 restores normal operation; limit_us alone (withhold_row = -1)
  * only shortens the limit.  Returns PI_ERR_INVALID_ARG for withhold_row < -1,
  * or for a withheld entry without a limit.  Not thread-safe; set it while no
