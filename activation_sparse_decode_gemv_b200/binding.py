@@ -167,9 +167,11 @@ def _c_int(n, what: str) -> int:
 
 def _tokens(u: torch.Tensor, d: int, what: str) -> int:
     """Batch size of a [B, d] token tensor."""
-    if u.dim() != 2 or u.shape[1] != d:
-        raise ValueError(f"{what}: shape {tuple(u.shape)}, expected [B, {d}]")
-    return _c_int(u.shape[0], f"{what}: rows")
+    shape = u.shape
+    if len(shape) != 2 or shape[1] != d:
+        raise ValueError(f"{what}: shape {tuple(shape)}, expected [B, {d}]")
+    n = shape[0]
+    return n if n < 2 ** 31 else _c_int(n, f"{what}: rows")
 
 
 def _need_ws(ws: torch.Tensor):
@@ -361,11 +363,11 @@ def _ptrs(names: str, *tensors: Optional[torch.Tensor]):
     return out
 
 
-def _check_moved(names, tensors, at):
-    """The tensors whose addresses a handle or a description holds still lie there: their values may change in
-    place, but one that was given other memory (w.data = ...) would be read where it was."""
-    for what, t, p in zip(names, tensors, at):
-        if t is not None and t.data_ptr() != p:
+def _check_moved(kept):
+    """The tensors whose addresses a handle or a description holds, as (name, tensor, address), still lie there: their
+    values may change in place, but one that was given other memory (w.data = ...) would be read where it was."""
+    for what, t, p in kept:
+        if t.data_ptr() != p:
             raise ValueError(f"{what}: its memory has moved since the layer or norm was made; make a new one")
 
 
@@ -418,15 +420,12 @@ class GatedFfnLayer:
             if t.device != w_gate.device:
                 raise ValueError(f"{what}: on {t.device}, w_gate is on {w_gate.device}")
         self._keep = (w_gate, w_up, w_down_t)
-        self._at = tuple(t.data_ptr() for t in self._keep)
+        self._kept = tuple((n, t, t.data_ptr()) for n, t in zip(("w_gate", "w_up", "w_down_t"), self._keep))
         self.desc = pi_gated_ffn_desc(self.d, self.f, GATE_ACT[act], DTYPE[self.dtype], _p(w_gate), _p(w_up),
                                       _p(w_down_t))
         h = C.c_void_p()
         _check(lib().pi_gated_ffn_create(C.byref(self.desc), C.byref(h)), "pi_gated_ffn_create")
         self.handle = h
-
-    def _check_weights(self):
-        _check_moved(("w_gate", "w_up", "w_down_t"), self._keep, self._at)
 
     def close(self):
         if getattr(self, "handle", None):
@@ -456,7 +455,7 @@ def pi_gated_ffn_forward(layer: GatedFfnLayer, u: torch.Tensor, y: torch.Tensor,
                          gate: Optional[torch.Tensor] = None, up: Optional[torch.Tensor] = None, stream=None):
     """u [T, d] -> y [T, d]; gate, up: optional outputs [T, f] (the pre-activations)."""
     T = _tokens(u, layer.d, "u")
-    layer._check_weights()
+    _check_moved(layer._kept)
     _check_out(u, "u", layer.dtype, (T, layer.d))
     _check_out(y, "y", layer.dtype, (T, layer.d))
     _check_out(gate, "gate", layer.dtype, (T, layer.f))
@@ -474,7 +473,7 @@ def pi_gated_ffn_backward(layer: GatedFfnLayer, u: torch.Tensor, gate: torch.Ten
     """Gradients at a forward call's u, gate and up, for dy [T, d].  du [T, d];
     dw_* [f, d], all fp32 or all of the layer's type; each may be left out."""
     T = _tokens(u, layer.d, "u")
-    layer._check_weights()
+    _check_moved(layer._kept)
     for what, t in (("u", u), ("dy", dy), ("du", du)):
         _check_out(t, what, layer.dtype, (T, layer.d))
     for what, t in (("gate", gate), ("up", up)):
@@ -513,14 +512,18 @@ class BlockNorm:
         self.d, self.y_dtype, self.u_dtype, self.post_norm = d, y_dtype, u_dtype, bool(post_norm)
         self.gate, self.tokens_per_gate = gate, tokens_per_gate
         self.w_post, self.w_pre = w_post, w_pre
-        self._at = tuple(None if t is None else t.data_ptr() for t in (w_post, w_pre, gate))
+        self._kept = tuple((n, t, t.data_ptr()) for n, t in (("w_post", w_post), ("w_pre", w_pre), ("gate", gate))
+                           if t is not None)
+        # one of them per device, for the check of devices (what has not moved is on the device where it was)
+        lead = {t.device: (n, t) for n, t, _ in self._kept}.values()
+        self._lead_names, self._lead = " ".join(n for n, _ in lead), tuple(t for _, t in lead)
         self.desc = pi_block_norm_desc(d, DTYPE[y_dtype], DTYPE[u_dtype], int(post_norm), eps, residual_scale,
                                        branch_scale, _p(w_post), _p(w_pre), _p(gate), tokens_per_gate)
         self.ref = C.byref(self.desc)
 
     def _check_tokens(self, T: int):
         """The gate has a row for each of T tokens, and the parameters lie where they did."""
-        _check_moved(("w_post", "w_pre", "gate"), (self.w_post, self.w_pre, self.gate), self._at)
+        _check_moved(self._kept)
         if self.gate is not None and self.gate.shape[0] * self.tokens_per_gate < T:
             raise ValueError(f"gate: {self.gate.shape[0]} rows of {self.tokens_per_gate} tokens for {T} tokens")
 
@@ -539,8 +542,8 @@ def pi_block_norm_forward(norm: BlockNorm, x: torch.Tensor, y: Optional[torch.Te
     _check_out(u, "u", norm.u_dtype, (T, norm.d))
     _check_out(rstd_post, "rstd_post", torch.float32, (T,))
     _check_out(rstd_pre, "rstd_pre", torch.float32, (T,))
-    px, py, po, pu, pk, pr, *_ = _ptrs("x y x_out u rstd_post rstd_pre w_post w_pre gate", x, y, x_out, u, rstd_post,
-                                       rstd_pre, norm.w_post, norm.w_pre, norm.gate)
+    px, py, po, pu, pk, pr, *_ = _ptrs("x y x_out u rstd_post rstd_pre " + norm._lead_names, x, y, x_out, u, rstd_post,
+                                       rstd_pre, *norm._lead)
     _check(lib().pi_block_norm_forward(norm.ref, px, py, T, po, pu, pk, pr, _raw_stream(stream)),
            "pi_block_norm_forward")
 
@@ -585,8 +588,8 @@ def pi_block_norm_backward(norm: BlockNorm, x_out: Optional[torch.Tensor], y: Op
         _check_out(dgate, "dgate", torch.float32, norm.gate.shape)
     n = _ws_bytes(ws)
     (pr, py, pkp, pkr, pdu, pg, pdx, pdy, pw, p0, p1, p2, *_) = _ptrs(
-        "x_out y rstd_post rstd_pre du dx_out dx dy workspace dw_post dw_pre dgate w_post w_pre gate", x_out, y,
-        rstd_post, rstd_pre, du, dx_out, dx, dy, ws, dw_post, dw_pre, dgate, norm.w_post, norm.w_pre, norm.gate)
+        "x_out y rstd_post rstd_pre du dx_out dx dy workspace dw_post dw_pre dgate " + norm._lead_names, x_out, y,
+        rstd_post, rstd_pre, du, dx_out, dx, dy, ws, dw_post, dw_pre, dgate, *norm._lead)
     _check(lib().pi_block_norm_backward(norm.ref, pr, py, pkp, pkr, pdu, pg, T, pdx, pdy, p0, p1, p2, int(flags), pw,
                                         n, _raw_stream(stream)), "pi_block_norm_backward")
 
