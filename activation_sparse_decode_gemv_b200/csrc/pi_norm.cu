@@ -154,11 +154,12 @@ pi_status pi_block_norm_forward(const pi_block_norm_desc *desc, const float *x, 
   if (overlapping(mem, 4, 9)) return PI_ERR_INVALID_ARG;
   NM::FwdArgs a{};
   a.x = x, a.y = y;
-  a.w_post = desc->w_post, a.w_pre = desc->w_pre, a.gate = desc->gate;
+  a.w_pre = desc->w_pre;
+  if (y) a.w_post = desc->w_post, a.gate = desc->gate;  // without a branch nothing of it enters r
   a.x_out = x_out, a.u = u, a.rstd_post = rstd_post, a.rstd_pre = rstd_pre;
   a.tokens = tokens, a.d = desc->d_model;
   a.tokens_per_gate = desc->tokens_per_gate < tokens ? desc->tokens_per_gate : tokens;
-  a.y_type = desc->y_dtype, a.u_type = desc->u_dtype, a.post_norm = desc->post_norm ? 1 : 0;
+  a.y_type = desc->y_dtype, a.u_type = desc->u_dtype, a.post_norm = y && desc->post_norm ? 1 : 0;
   a.eps = desc->eps, a.alpha = desc->residual_scale, a.beta = desc->branch_scale;
   const int sms = device_sm_count();
   if (sms <= 0) return PI_ERR_CUDA;

@@ -320,3 +320,19 @@ def test_an_explicit_stream(cuda_device):
     assert torch.all(early == 0)
     side.synchronize()
     assert torch.equal(u, want)
+
+
+# ---------------------------------------------------------------- no branch
+@pytest.mark.parametrize("T,d", [(5, 264), (3, 8200)])
+@pytest.mark.parametrize("bad", [NAN, INF])
+def test_without_a_branch_its_parameters_are_not_used(cuda_device, T, d, bad):
+    """y = None: r = residual_scale x, whatever the branch's gate and weights hold."""
+    gate, w = torch.full((T, d), bad, device="cuda"), torch.full((d,), bad, device="cuda")
+    norm = pb.BlockNorm(d, y_dtype=F32, u_dtype=F32, post_norm=True, w_post=w, gate=gate, tokens_per_gate=1,
+                        residual_scale=2.0, branch_scale=0.5)
+    plain = pb.BlockNorm(d, u_dtype=F32, residual_scale=2.0)
+    x = torch.randn(T, d, device="cuda")
+    r, u, r0, u0 = (_e(T, d) for _ in range(4))
+    pb.pi_block_norm_forward(norm, x, None, r, u)
+    pb.pi_block_norm_forward(plain, x, None, r0, u0)
+    assert torch.equal(r, 2 * x) and torch.equal(u, u0) and torch.equal(r, r0)
