@@ -413,18 +413,19 @@ PI_DEV void put_row4(const Args &a, void *out, int m, int n, const float (&v)[4]
 
 template <int NC>
 PI_DEV void epi_i8(const Args &a, int m, int n0, const float (&v)[NC]) {
-  const float sm = m < a.m ? __ldg(a.s_m + m) : 0.f;
-  const float b = m < a.m && a.bias ? __ldg(a.bias + m) : 0.f;
+  // scales may come from the kernel before this one, under which this one starts: no non-coherent loads
+  const float sm = m < a.m ? a.s_m[m] : 0.f;
+  const float b = m < a.m && a.bias ? a.bias[m] : 0.f;
   float o[NC], sn[NC];
   if (NC % 4 == 0 && n0 + NC <= a.n) {
 #pragma unroll
     for (int j = 0; j + 3 < NC; j += 4) {
-      const float4 f = __ldg(reinterpret_cast<const float4 *>(a.s_n + n0 + j));
+      const float4 f = *reinterpret_cast<const float4 *>(a.s_n + n0 + j);
       sn[j] = f.x, sn[j + 1] = f.y, sn[j + 2] = f.z, sn[j + 3] = f.w;
     }
   } else {
 #pragma unroll
-    for (int j = 0; j < NC; ++j) sn[j] = __ldg(a.s_n + min(n0 + j, a.n - 1));
+    for (int j = 0; j < NC; ++j) sn[j] = a.s_n[min(n0 + j, a.n - 1)];
   }
 #pragma unroll
   for (int j = 0; j < NC; ++j) o[j] = fmaf((float)__float_as_int(v[j]) * sn[j], sm, b);
@@ -1018,11 +1019,11 @@ __global__ void __launch_bounds__(kSplitThreads, 2) split_gemm_kernel(const __gr
         if (a.up_out) put_row4<T>(a, a.up_out, m, n, w);
         put_row4<T>(a, a.out[0], m, n, o);
       } else if constexpr (EPI == E_I8) {
-        const float sn = __ldg(a.s_n + n);
+        const float sn = a.s_n[n];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int mj = min(m + j, a.m - 1);
-          v[j] = fmaf((float)__float_as_int(v[j]) * sn, __ldg(a.s_m + mj), a.bias ? __ldg(a.bias + mj) : 0.f);
+          v[j] = fmaf((float)__float_as_int(v[j]) * sn, a.s_m[mj], a.bias ? a.bias[mj] : 0.f);
         }
         if (a.out_type == O_F32) put_row4<float>(a, a.out[0], m, n, v);
         else if (a.out_type == O_F16) put_row4<__half>(a, a.out[0], m, n, v);

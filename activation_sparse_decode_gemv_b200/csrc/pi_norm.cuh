@@ -452,8 +452,8 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const BwdArgs a) {
 #pragma unroll
   for (int k = 0; k < R; ++k) fetch(t0 + k, k);
   const bool post = a.y && a.post_norm;
-  auto rr_of = [&](int t) { return a.du ? __ldg(a.rstd_pre + t) : 0.f; };
-  auto rp_of = [&](int t) { return post ? __ldg(a.rstd_post + t) : 1.f; };
+  auto rr_of = [&](int t) { return a.du ? a.rstd_pre[t] : 0.f; };
+  auto rp_of = [&](int t) { return post ? a.rstd_post[t] : 1.f; };
   auto col = [&](int c) { return col0 + (int)(threadIdx.x + c * step) * 4; };
   auto factor = [&](const float *gate_row, int c) {
     return valid >> c & 1u ? p4(branch_factor(gate_row, a.w_post, a.beta, col(c))) : p4(zero4());

@@ -1,8 +1,10 @@
-"""A block may touch another block's shared memory only once that block has
+"""Orders that the kernels of the dense operators rely on, read from their source
+on the CPU.
+
+A block may touch another block's shared memory only once that block has
 started, which a cluster barrier that every block has passed shows (being
-launched together does not).  On the CPU, from the kernels' source: in each
-kernel that reaches a peer's shared memory, a cluster barrier is waited for
-before the first such access."""
+launched together does not): in each kernel that reaches a peer's shared
+memory, a cluster barrier is waited for before the first such access."""
 import os
 import re
 
@@ -49,3 +51,11 @@ def test_the_wait_has_its_arrival():
         if "peer_started_wait<CL>()" in body:
             assert body.index("peer_started_arrive<CL>()") < body.index("peer_started_wait<CL>()") \
                 < body.index("for (int t = t0; t < t1; ++t)"), k
+
+
+@pytest.mark.parametrize("name", ["pi_norm.cuh", "pi_gemm.cuh"])
+def test_no_non_coherent_loads(name):
+    """These kernels start under the one before them, which may still be writing what they read after their wait
+    (factors, scales).  A non-coherent load is for memory that nothing writes while the kernel lives."""
+    text = re.sub(r"//[^\n]*", "", open(os.path.join(CSRC, name)).read())
+    assert "__ldg(" not in text and "ld.global.nc" not in text and "ld_stream" not in text and "ld_keep" not in text
