@@ -347,6 +347,14 @@ def _check_out(t: Optional[torch.Tensor], what: str, dtype, shape):
         raise ValueError(f"{what}: must be contiguous")
 
 
+def _check_in(t: torch.Tensor, what: str, dtype):
+    """A contiguous tensor whose shape _tokens has checked."""
+    if t.dtype != dtype:
+        raise ValueError(f"{what}: dtype {t.dtype}, expected {dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what}: must be contiguous")
+
+
 def _ptrs(names: str, *tensors: Optional[torch.Tensor]):
     """The tensors' addresses (None stays None).  All of them on the current
     CUDA device: kernels launch there, on its current stream."""
@@ -456,7 +464,7 @@ def pi_gated_ffn_forward(layer: GatedFfnLayer, u: torch.Tensor, y: torch.Tensor,
     """u [T, d] -> y [T, d]; gate, up: optional outputs [T, f] (the pre-activations)."""
     T = _tokens(u, layer.d, "u")
     _check_moved(layer._kept)
-    _check_out(u, "u", layer.dtype, (T, layer.d))
+    _check_in(u, "u", layer.dtype)
     _check_out(y, "y", layer.dtype, (T, layer.d))
     _check_out(gate, "gate", layer.dtype, (T, layer.f))
     _check_out(up, "up", layer.dtype, (T, layer.f))
@@ -536,7 +544,7 @@ def pi_block_norm_forward(norm: BlockNorm, x: torch.Tensor, y: Optional[torch.Te
     and the next block's input u [T, d]; rstd_post, rstd_pre: optional fp32 [T]."""
     T = _tokens(x, norm.d, "x")
     norm._check_tokens(T)
-    _check_out(x, "x", torch.float32, (T, norm.d))
+    _check_in(x, "x", torch.float32)
     _check_out(y, "y", norm.y_dtype, (T, norm.d))
     _check_out(x_out, "x_out", torch.float32, (T, norm.d))
     _check_out(u, "u", norm.u_dtype, (T, norm.d))
