@@ -128,14 +128,15 @@ struct Tilings {
   double epilogue;
 };
 // 160 to 224 columns waste fewer of the last tile's where tokens are not a
-// multiple of 256: with them 619 tokens of 8128 x 28176 take 681 us, without 741
+// multiple of 256: with them 619 tokens of 8128 x 28176 take 741 to 773 us (bf16
+// normal values), without 856
 constexpr Tilings kGluTilings{5, {{2, 256}, {2, 224}, {2, 192}, {2, 160}, {2, 128}}, 9000};
 constexpr Tilings kDgluTilings{5, {{1, 256}, {1, 224}, {1, 192}, {1, 160}, {1, 128}}, 10000};
 constexpr Tilings kStoreTilings{
     8, {{2, 256}, {2, 224}, {2, 192}, {2, 160}, {1, 256}, {1, 192}, {1, 160}, {1, 128}}, 6000};
 constexpr Tilings kWeightTilings{2, {{2, 256}, {1, 256}}, 6000};
 // {2, 256} measured 10% slower (4096 x 5120 x 13824: 245 us, 224); 430 tokens of
-// 4096 x 11008: 28.7 us with 160 to 224 columns, 31.4 without
+// 4096 x 11008: 28.3 us with 160 to 224 columns, 31.4 without
 constexpr Tilings kI8Tilings{5, {{1, 256}, {1, 224}, {1, 192}, {1, 160}, {1, 128}}, 7000};
 
 const Tilings &tilings_of(int product) {
@@ -153,7 +154,11 @@ constexpr int kSplits[] = {1, 2, 4, 5, 6, 8};
 // Test support (pi_debug_dense_plan): the tiling that a product's calls use; nt = 0: the rule's.
 Plan g_forced[kProducts];
 
-// Estimated SM cycles of the two kernels.  A tiling's K blocks cost the slower
+// Estimated SM cycles of the two kernels, to rank tilings by.  Their constants,
+// and the epilogues' cycles above, are fitted, so that the rule takes the fastest
+// tiling or one within 10% of it in forced sweeps of 18 products (16 to 4096
+// tokens, 16 and 8 bits); they are no measured rates (at 300 tokens of 4096 x
+// 11008 an SM draws 37 to 40 B a cycle).  A tiling's K blocks cost the slower
 // of the MMAs (2 cycles a column and block), the arrival of its bytes at the
 // SMs' share of the L2 (about 6 KB a cycle in all, 60 B at most for one SM) and,
 // for the split kernel, the latency of a load over the ring's depth.

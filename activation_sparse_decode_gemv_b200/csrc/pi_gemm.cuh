@@ -20,8 +20,10 @@
 //                      two 256-row blocks x NT columns, persistent; the
 //                      epilogue of a tile runs under the next tile's MMAs
 //                      (two accumulator buffers), or half of it does (one).
-//                      In isolation the tensor pipe is 85% active (gate | up
-//                      product of 4096 x 5120 x 13824, 16 bits); back to back
+//                      In isolation the tensor pipe is 79% active (gate | up
+//                      product of 4096 x 5120 x 13824, 16 bits; 84% in the
+//                      weights' gradients, 89 and 93% in y and du; 78% in the
+//                      8-bit product of 2011 tokens); back to back
 //                      the 1000 W power cap bounds it: 1.31 PFLOP/s for 2048 x
 //                      8192 x 28672 against 1.28 for three library products,
 //                      where the L2 traffic of a block that each B tile
@@ -29,7 +31,7 @@
 //   split_gemm_kernel  few tokens: 128 x NT tiles, K split over a cluster's
 //                      CTAs, partial sums joined through distributed shared
 //                      memory in rank order (no workspace, no atomics).
-//                      Bound by HBM: 5.9 TB/s of weights at one token, 5.2 at
+//                      Bound by HBM: 5.9 TB/s of weights at one token, 5.3 at
 //                      45 (5120 x 13824, 4096 x 16384); a small product is
 //                      about 6 us, of which 0.7 set-up, 0.7 first load, 1 each
 //                      cluster barrier, 1 to 3 the join.

@@ -3,8 +3,8 @@
 // of the 8-bit product.  All are bound by HBM: each reads its inputs once and
 // writes its outputs once, with every sum and statistic in fp32.  Measured
 // (bf16 y and u): forward of 8192 x 5120 90.9 us, 5.5 TB/s; gradients of 4096 x
-// 7168 109 us, 4.8 TB/s, of which 96 the rows and 8 the joining kernel; one token
-// of 8192 3.6 us (a launch).
+// 7168 109 us, 4.8 TB/s, of which about 96 the row kernel and 13 the joining one
+// (alone, with cold caches, 100 and 14); one token of 8192 3.6 us (a launch).
 #pragma once
 
 #include <cuda_bf16.h>

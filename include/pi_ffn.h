@@ -238,18 +238,21 @@ pi_status pi_debug_wait_fault(int withhold_row, unsigned limit_us);
  *
  * Conventions: those at the top of this file, and
  *  - every tensor is contiguous and 16-byte aligned; token counts may be 0
- *    (per-token pointers may then be NULL, nothing is read, and gradients that
- *    sum over tokens are set to zero) and are at most 2^24; outputs overlap no
- *    input and no other output unless stated;
+ *    (per-token pointers may then be NULL, nothing is read, and gradients of
+ *    weights, which sum over tokens, are set to zero) and are at most 2^24;
+ *    outputs overlap no input and no other output unless stated;
  *  - products accumulate in fp32 (int32 for 8-bit codes), and norms, gates
  *    and their statistics are fp32; a value is rounded where it is stored;
  *  - results do not depend on timing: every sum has a fixed order;
- *  - non-finite inputs give non-finite results in the rows (for gradients of
- *    weights, the columns) that they enter, and touch no others;
+ *  - non-finite inputs give non-finite results in the rows that they enter (for
+ *    gradients of weights, the rows or columns), and touch no others.  A norm
+ *    whose sum of squares lies past fp32's range (3.4e38) has factor 0;
  *  - a workspace's first 256 bytes must be zero before its first use
  *    (pi_workspace_init, or any memset of them); it belongs to one call at a
  *    time.  The bounded waits of these kernels report PI_ERR_TIMEOUT through
- *    pi_get_device_status(ws). */
+ *    pi_get_device_status(ws);
+ *  - calls may come from any host thread, several at once with workspaces and
+ *    outputs of their own, and may be captured, a process's first ones too. */
 typedef enum pi_dtype { PI_DT_F32 = 0, PI_DT_F16 = 1, PI_DT_BF16 = 2 } pi_dtype;
 
 /* phi(g): SiLU g / (1 + e^-g); ReLU max(g, 0), slope 0 at 0; GELU
@@ -314,8 +317,10 @@ typedef struct pi_block_norm_desc {
 } pi_block_norm_desc;
 
 /* x [tokens x d] -> x_out (r; may be x itself) and u, at least one of them.
- * y may be NULL: r = residual_scale x.  rstd_post, rstd_pre: optional outputs
- * [tokens], the factors 1 / sqrt(mean + eps), which the backward pass takes. */
+ * y may be NULL: r = residual_scale x, whatever the branch's parameters hold.
+ * rstd_post, rstd_pre: optional outputs [tokens], the factors 1 / sqrt(mean +
+ * eps), which the backward pass takes (rstd_post with y and post_norm only,
+ * rstd_pre with u only). */
 pi_status pi_block_norm_forward(const pi_block_norm_desc *desc, const float *x, const void *y, int tokens,
                                 float *x_out, void *u, float *rstd_post, float *rstd_pre, pi_stream_t stream);
 
@@ -325,7 +330,9 @@ pi_status pi_block_norm_workspace_size(const pi_block_norm_desc *desc, int max_t
  * used) and dx_out, the gradient that reaches the new stream by other ways
  * (NULL: none); at least one of the two.  dx [tokens x d] fp32 (may be dx_out
  * itself), dy [tokens x d] in y_dtype (may be y itself), dw_post, dw_pre [d] and
- * dgate (the gate's shape) fp32; each may be NULL.  flags: PI_GRAD_ACCUMULATE
+ * dgate fp32; each may be NULL (dw_pre needs du; dy, dw_post and dgate need y).
+ * dgate has the gate's shape, [ceil(tokens / tokens_per_gate) x d]; what a longer
+ * buffer holds behind those rows is left as it was.  flags: PI_GRAD_ACCUMULATE
  * (dw_post, dw_pre, dgate). */
 pi_status pi_block_norm_backward(const pi_block_norm_desc *desc, const float *x_out, const void *y,
                                  const float *rstd_post, const float *rstd_pre, const void *du, const float *dx_out,
